@@ -1,0 +1,336 @@
+"""Cases of the framework's operators for rounded layers: fp8 quantisation by blocks, products in fp8, products
+grouped by expert with their gradients, and token log probabilities with their gradient.
+
+`own = False` computes the plain forms with elementary torch operations in 32 bits; `own = True` makes the calls of
+`two_sided_gptq_amd.bakron`.  Inputs follow `two_sided_gptq_amd/synth.py`'s distributions (weights N(0, 0.02^2),
+activations N(0, 1) with a few channels of 20 times the size).
+"""
+import math
+
+import torch
+
+own = False
+
+BLOCK = 128
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+SIZE = {"f32": 4, "bf16": 2, "f16": 2}
+
+
+def listed():
+    return [
+        # activations of one token of a 14336-wide layer on their way into an fp8 product
+        {"name": "quantize_token", "op": "fp8_quantize", "rows": 1, "cols": 14336, "dtype": "bf16", "block_rows": 1},
+        # the activations of a long prompt
+        {"name": "quantize_prompt", "op": "fp8_quantize", "rows": 8191, "cols": 4096, "dtype": "bf16", "block_rows": 1},
+        # decoding one token through a 4096 x 14336 layer whose codes carry a scale for each row
+        {"name": "fp8_token", "op": "fp8_matmul", "rows": 1, "n": 4096, "k": 14336, "groups": 1, "skew": 0.0, "scale": "row", "out": "bf16"},
+        # a prompt through the same layer the other way round, weights scaled by 128 x 128 blocks
+        {"name": "fp8_prompt", "op": "fp8_matmul", "rows": 8192, "n": 14336, "k": 4096, "groups": 1, "skew": 0.0, "scale": "block", "out": "bf16"},
+        # a batch of prompts through rounded experts, unevenly routed, with row scales
+        {"name": "fp8_experts", "op": "fp8_matmul", "rows": 9001, "n": 4096, "k": 2048, "groups": 32, "skew": 1.0, "scale": "row", "out": "bf16"},
+        # decoding a batch of 32 tokens, two experts of 64 each: most experts see one token or none
+        {"name": "experts_tokens", "op": "grouped_matmul", "rows": 64, "n": 2048, "k": 1024, "groups": 64, "skew": 0.5, "dtype": "bf16"},
+        # prompts through 8 wide experts
+        {"name": "experts_prompt", "op": "grouped_matmul", "rows": 16384, "n": 11008, "k": 4096, "groups": 8, "skew": 0.3, "dtype": "bf16"},
+        # backward through the experts of a batch, the usual sizes
+        {"name": "experts_grad", "op": "grouped_matmul_grad", "rows": 8192, "n": 4096, "k": 2048, "groups": 16, "skew": 0.5, "dtype": "bf16"},
+        # backward through small experts with few, odd numbers of tokens and experts without any
+        {"name": "experts_grad_odd", "op": "grouped_matmul_grad", "rows": 1003, "n": 1000, "k": 520, "groups": 24, "skew": 1.5, "dtype": "f16"},
+        # the next token of a small batch: log probability, entropy and 20 alternatives
+        {"name": "logprobs_tokens", "op": "token_logprobs", "rows": 8, "vocab": 131072, "top": 20, "dtype": "bf16", "masked": True},
+        # scoring a text: a vocabulary of odd size, 32-bit logits, some of them masked
+        {"name": "logprobs_text", "op": "token_logprobs", "rows": 4096, "vocab": 50001, "top": 5, "dtype": "f32", "masked": True},
+        # the gradient of such scores, with an entropy term
+        {"name": "logprobs_grad", "op": "token_logprobs_grad", "rows": 4096, "vocab": 131072, "dtype": "bf16", "masked": False},
+    ]
+
+
+def _spread(rng, low, high, step=1):
+    """A size spread over its logarithm, a multiple of `step`."""
+    v = math.exp(rng.uniform(math.log(low), math.log(high)))
+    return max(step, int(round(v / step)) * step)
+
+
+def draw(rng):
+    op = rng.choice(["fp8_quantize", "fp8_matmul", "grouped_matmul", "grouped_matmul_grad", "token_logprobs", "token_logprobs_grad"])
+    if op == "fp8_quantize":
+        return {"op": op, "rows": _spread(rng, 1, 8192), "cols": _spread(rng, 100, 14336, rng.choice([1, 16])),
+                "dtype": rng.choice(["f32", "bf16", "f16"]), "block_rows": rng.choice([1, 1, 128])}
+    if op in ("token_logprobs", "token_logprobs_grad"):
+        case = {"op": op, "rows": _spread(rng, 1, 4096), "vocab": _spread(rng, 1000, 131072, rng.choice([1, 64])),
+                "dtype": rng.choice(["f32", "bf16", "f16"]), "masked": rng.random() < 0.5}
+        if op == "token_logprobs":
+            case["top"] = rng.choice([0, 1, 5, 20, 32])
+        return case
+    # most layers have widths that are multiples of 16; one in four here has not
+    step = rng.choice([16, 16, 16, 1])
+    n, k = _spread(rng, 64, 14336, step), _spread(rng, 64, 14336, step)
+    if op == "fp8_matmul":
+        groups = rng.choice([1, 1, _spread(rng, 2, 64)])
+        # no more weights than 2^30, and no more operations than the largest case
+        groups = max(1, min(groups, (1 << 30) // (n * k)))
+        rows = _spread(rng, 1, min(16384, 2 ** 39 // (n * k)))
+        return {"op": op, "rows": rows, "n": n, "k": k, "groups": groups, "skew": round(rng.uniform(0, 1.5), 2),
+                "scale": rng.choice(["row", "block"]), "out": rng.choice(["bf16", "bf16", "f32", "f16"])}
+    groups = max(1, min(_spread(rng, 2, 64), (1 << 28) // (n * k)))
+    rows = _spread(rng, 1, min(16384, 2 ** 38 // (n * k)))
+    return {"op": op, "rows": rows, "n": n, "k": k, "groups": groups, "skew": round(rng.uniform(0, 1.5), 2),
+            "dtype": rng.choice(["bf16", "bf16", "f16"])}
+
+
+def _counts(case, seed):
+    """How many rows each group has: shares that fall as 1 / rank^skew, in a random order, drawn at random."""
+    g = torch.Generator().manual_seed(seed * 7919 + 13)
+    share = torch.arange(1, case["groups"] + 1, dtype=torch.float64).pow(-case["skew"])
+    share = share[torch.randperm(case["groups"], generator=g)]
+    to = torch.multinomial(share, case["rows"], replacement=True, generator=g)
+    return torch.bincount(to, minlength=case["groups"])
+
+
+def _activations(rows, cols, gen):
+    x = torch.randn(rows, cols, device="cuda", generator=gen)
+    loud = torch.randint(0, cols, (max(1, cols // 128),), device="cuda", generator=gen)
+    x[:, loud] *= 20.0
+    return x
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    op = case["op"]
+    if op == "fp8_quantize":
+        x = _activations(case["rows"], case["cols"], gen)
+        return {"case": case, "x": x.to(DTYPES[case["dtype"]])}
+    if op == "fp8_matmul":
+        m, n, k, groups = case["rows"], case["n"], case["k"], case["groups"]
+        kb, nb = -(-k // BLOCK), -(-n // BLOCK)
+        # codes as a block quantiser leaves them, each block's largest near 448, and scales of ordinary sizes
+        x = _activations(m, k, gen).mul_(100.0).clamp_(-448, 448).to(torch.float8_e4m3fn)
+        sx = torch.rand(kb, m, device="cuda", generator=gen).mul_(0.02).add_(0.005)
+        shape = (groups, n, k) if groups > 1 else (n, k)
+        if case["scale"] == "row":  # a solver's 4-bit codes with the rows' scales
+            w = torch.randint(-7, 8, shape, device="cuda", generator=gen, dtype=torch.int8).to(torch.float8_e4m3fn)
+            sw = torch.rand(shape[:-1], device="cuda", generator=gen).mul_(0.01).add_(0.005)
+        else:
+            w = torch.empty(shape, device="cuda", dtype=torch.float8_e4m3fn)
+            w.copy_(torch.randn(shape, device="cuda", generator=gen).mul_(120.0).clamp_(-448, 448))
+            sw = torch.rand((*shape[:-2], kb, nb), device="cuda", generator=gen).mul_(2e-4).add_(5e-5)
+        state = {"case": case, "x": x, "sx": sx, "w": w, "sw": sw, "offsets": None, "bounds": [0, m]}
+        if groups > 1:
+            counts = _counts(case, seed)
+            at = torch.cat([torch.zeros(1, dtype=torch.int64), counts.cumsum(0)])
+            state |= {"offsets": at.to(torch.int32).cuda(), "bounds": at.tolist()}
+        return state
+    if op in ("grouped_matmul", "grouped_matmul_grad"):
+        t = DTYPES[case["dtype"]]
+        m, n, k, groups = case["rows"], case["n"], case["k"], case["groups"]
+        at = torch.cat([torch.zeros(1, dtype=torch.int64), _counts(case, seed).cumsum(0)])
+        state = {"case": case, "x": _activations(m, k, gen).to(t), "offsets": at.to(torch.int32).cuda(), "bounds": at.tolist(),
+                 "w": torch.randn(groups, n, k, device="cuda", generator=gen).mul_(0.02).to(t)}
+        if op == "grouped_matmul_grad":
+            state["dy"] = torch.randn(m, n, device="cuda", generator=gen).mul_(0.1).to(t)
+        return state
+    rows, vocab, t = case["rows"], case["vocab"], DTYPES[case["dtype"]]
+    x = torch.randn(rows, vocab, device="cuda", generator=gen).mul_(2.5)
+    # one token of each row stands out, as where a model is fairly sure
+    x[torch.arange(rows, device="cuda"), torch.randint(0, vocab, (rows,), device="cuda", generator=gen)] += 9.0
+    x = x.to(t)
+    targets = torch.randint(0, vocab, (rows,), device="cuda", generator=gen)
+    if case["masked"]:
+        x[::3, vocab // 2:vocab // 2 + vocab // 10] = -math.inf  # a vocabulary's unused part
+        x[1::5, ::2] = torch.finfo(t).min  # a grammar that forbids tokens
+        targets = 2 * (targets % (vocab // 4)) + 1  # no target is a masked token
+        targets[2::7] = -1  # rows without a target
+    state = {"case": case, "logits": x, "targets": targets}
+    if op == "token_logprobs_grad":
+        # the forward pass's results, which the backward pass starts from
+        y = x.float()
+        top = y.amax(1, keepdim=True)
+        e = (y - top).exp()
+        s = e.sum(1, keepdim=True)
+        state["lse"] = (s.log() + top).squeeze(1)
+        state["entropy"] = (s.log() - torch.where(e > 0, e * (y - top), 0.0).sum(1, keepdim=True) / s).squeeze(1)
+        state["g"] = torch.randn(rows, device="cuda", generator=gen) / rows
+        state["gh"] = torch.randn(rows, device="cuda", generator=gen) * (0.1 / rows)
+    return state
+
+
+def _plain_quantize(state):
+    case, x = state["case"], state["x"].float()
+    rows, cols = x.shape
+    br, nb, kb = case["block_rows"], -(-rows // case["block_rows"]), -(-cols // BLOCK)
+    full = torch.zeros(nb * br, kb * BLOCK, device=x.device)
+    full[:rows, :cols] = x
+    amax = full.view(nb, br, kb, BLOCK).abs().amax(dim=(1, 3))
+    amax = torch.where(amax > 0, amax.clamp(min=2.0 ** -100), 448.0)  # a block of zeros has the scale 1
+    inv = 448.0 / amax
+    q = (full.view(nb, br, kb, BLOCK) * inv[:, None, :, None]).clamp(-448.0, 448.0)
+    q = q.reshape(nb * br, kb * BLOCK)[:rows, :cols].to(torch.float8_e4m3fn)
+    return {"q": q, "scales": (amax / 448.0).t().contiguous()}
+
+
+def _plain_fp8(state):
+    case = state["case"]
+    x = state["x"].float()
+    x = x * state["sx"].t().repeat_interleave(BLOCK, 1)[:, :x.shape[1]]
+    w = state["w"].float()
+    if case["scale"] == "row":
+        w = w * state["sw"].unsqueeze(-1)
+    else:
+        s = state["sw"].transpose(-1, -2).repeat_interleave(BLOCK, -1).repeat_interleave(BLOCK, -2)
+        w = w * s[..., :w.shape[-2], :w.shape[-1]]
+    if state["offsets"] is None:
+        y = x @ w.t()
+    else:
+        at = state["bounds"]
+        y = torch.cat([x[a:b] @ w[g].t() for g, (a, b) in enumerate(zip(at, at[1:]))])
+    return y.to(DTYPES[case["out"]])
+
+
+def _plain_grouped(state):
+    x, w, at = state["x"].float(), state["w"].float(), state["bounds"]
+    y = torch.cat([x[a:b] @ w[g].t() for g, (a, b) in enumerate(zip(at, at[1:]))])
+    return y.to(state["x"].dtype)
+
+
+def _plain_grouped_grad(state):
+    x, w, dy, at = state["x"].float(), state["w"].float(), state["dy"].float(), state["bounds"]
+    dx = torch.cat([dy[a:b] @ w[g] for g, (a, b) in enumerate(zip(at, at[1:]))])
+    dw = torch.stack([dy[a:b].t() @ x[a:b] for a, b in zip(at, at[1:])])
+    return {"dx": dx.to(state["x"].dtype), "dw": dw.to(state["x"].dtype)}
+
+
+def _plain_logprobs(state):
+    case, x, targets = state["case"], state["logits"].float(), state["targets"]
+    top = x.amax(1, keepdim=True)
+    d = x - top
+    e = d.exp()
+    s = e.sum(1, keepdim=True)
+    lse = s.log() + top
+    at = x.gather(1, targets.clamp(min=0)[:, None]) - lse
+    out = {"logprob": torch.where(targets >= 0, at.squeeze(1), 0.0), "lse": lse.squeeze(1),
+           "entropy": (s.log() - torch.where(e > 0, e * d, 0.0).sum(1, keepdim=True) / s).squeeze(1)}
+    if case["top"]:
+        v, i = torch.sort(x, dim=1, descending=True, stable=True)  # equal values: the lowest index first
+        out["top_ids"] = i[:, :case["top"]].contiguous()
+        out["top_logprob"] = v[:, :case["top"]] - lse
+    return out
+
+
+def _plain_logprobs_grad(state):
+    x, targets = state["logits"].float(), state["targets"]
+    lp = x - state["lse"][:, None]
+    p = lp.exp()
+    g = torch.where(targets >= 0, state["g"], 0.0)
+    dx = -g[:, None] * p - state["gh"][:, None] * torch.where(p > 0, p * (lp + state["entropy"][:, None]), 0.0)
+    dx.scatter_add_(1, targets.clamp(min=0)[:, None], g[:, None])
+    return dx.to(state["logits"].dtype)
+
+
+def run(state):
+    case, op = state["case"], state["case"]["op"]
+    if own:
+        from two_sided_gptq_amd import bakron
+        if op == "fp8_quantize":
+            q, scales = bakron.fp8_quantize(state["x"], block_rows=case["block_rows"])
+            return {"q": q, "scales": scales}
+        if op == "fp8_matmul":
+            return bakron.fp8_matmul(state["x"], state["sx"], state["w"], state["sw"], offsets=state["offsets"], out_dtype=DTYPES[case["out"]])
+        if op == "grouped_matmul":
+            return bakron.grouped_matmul(state["x"], state["w"], state["offsets"])
+        if op == "grouped_matmul_grad":
+            dx, dw = bakron.grouped_matmul_grad(state["dy"], state["x"], state["w"], state["offsets"])
+            return {"dx": dx, "dw": dw}
+        if op == "token_logprobs":
+            out = bakron.token_logprobs(state["logits"], state["targets"], top=case["top"])
+            return {k: v for k, v in out.items() if v is not None}
+        return bakron.token_logprobs_grad(state["logits"], state["targets"], state["lse"], state["entropy"], state["g"], state["gh"])
+    return {"fp8_quantize": _plain_quantize, "fp8_matmul": _plain_fp8, "grouped_matmul": _plain_grouped,
+            "grouped_matmul_grad": _plain_grouped_grad, "token_logprobs": _plain_logprobs,
+            "token_logprobs_grad": _plain_logprobs_grad}[op](state)
+
+
+def work(case):
+    op = case["op"]
+    if op == "fp8_quantize":
+        e = case["rows"] * case["cols"]
+        blocks = -(-case["rows"] // case["block_rows"]) * -(-case["cols"] // BLOCK)
+        return {"bytes": e * (SIZE[case["dtype"]] + 1) + 4 * blocks, "flops": 3 * e}
+    if op in ("token_logprobs", "token_logprobs_grad"):
+        e, b = case["rows"] * case["vocab"], SIZE[case["dtype"]]
+        if op == "token_logprobs":
+            return {"bytes": e * b + case["rows"] * (20 + 12 * case["top"]), "flops": 5 * e}
+        return {"bytes": 2 * e * b + case["rows"] * 24, "flops": 8 * e}
+    m, n, k, groups = case["rows"], case["n"], case["k"], case["groups"]
+    # the weights of the groups that have rows: what a draw of the rows hits on average
+    share = [r ** -case["skew"] for r in range(1, groups + 1)]
+    used = sum(1.0 - (1.0 - s / sum(share)) ** m for s in share)
+    if op == "fp8_matmul":
+        kb, nb = -(-k // BLOCK), -(-n // BLOCK)
+        scales = 4 * (kb * m + used * (n if case["scale"] == "row" else kb * nb))
+        return {"bytes": m * k + used * n * k + scales + m * n * SIZE[case["out"]], "flops": 2 * m * n * k}
+    if op == "grouped_matmul":
+        return {"bytes": 2 * (m * k + used * n * k + m * n), "flops": 2 * m * n * k}
+    # dY, X and W read; dX and the whole dW written
+    return {"bytes": 2 * (m * n + 2 * m * k + used * n * k + groups * n * k), "flops": 4 * m * n * k}
+
+
+def exact(case, seed):
+    """The same outputs from their definitions in 64 bits."""
+    state, op = prepare(case, seed), case["op"]
+    if op == "fp8_quantize":
+        x, br = state["x"].double(), case["block_rows"]
+        rows, cols = x.shape
+        r, c = torch.arange(rows, device="cuda") // br, torch.arange(cols, device="cuda") // BLOCK
+        per_row = torch.zeros(rows, int(c[-1]) + 1, device="cuda", dtype=torch.float64)
+        per_row.index_reduce_(1, c, x.abs(), "amax")
+        amax = torch.zeros(int(r[-1]) + 1, int(c[-1]) + 1, device="cuda", dtype=torch.float64)
+        amax.index_reduce_(0, r, per_row, "amax")
+        scales = torch.where(amax > 0, amax.clamp(min=2.0 ** -100) / 448, 1.0)
+        return {"q": x / scales[r][:, c], "scales": scales.t()}
+    if op == "fp8_matmul":
+        x, w = state["x"].double(), state["w"].double()
+        at = state["bounds"]
+        w, sw = (w[None], state["sw"][None]) if w.dim() == 2 else (w, state["sw"])
+        y = torch.zeros(case["rows"], case["n"], device="cuda", dtype=torch.float64)
+        col = torch.arange(case["k"], device="cuda") // BLOCK
+        row = torch.arange(case["n"], device="cuda") // BLOCK
+        xs = x * state["sx"].double()[col].t()
+        for g in range(len(at) - 1):
+            s = sw[g].double()
+            wg = w[g] * (s[:, None] if case["scale"] == "row" else s[col][:, row].t())
+            y[at[g]:at[g + 1]] = xs[at[g]:at[g + 1]] @ wg.t()
+        return y
+    if op in ("grouped_matmul", "grouped_matmul_grad"):
+        x, w, at = state["x"].double(), state["w"].double(), state["bounds"]
+        if op == "grouped_matmul":
+            y = torch.zeros(case["rows"], case["n"], device="cuda", dtype=torch.float64)
+            for g in range(len(at) - 1):
+                y[at[g]:at[g + 1]] = x[at[g]:at[g + 1]] @ w[g].t()
+            return y
+        dy = state["dy"].double()
+        dx, dw = torch.zeros_like(x), torch.zeros_like(w)
+        for g in range(len(at) - 1):
+            a, b = at[g], at[g + 1]
+            dx[a:b] = dy[a:b] @ w[g]
+            dw[g] = dy[a:b].t() @ x[a:b]
+        return {"dx": dx, "dw": dw}
+    x, targets = state["logits"].double(), state["targets"]
+    lse = torch.logsumexp(x, 1)
+    lp = x - lse[:, None]
+    p = lp.exp()
+    hit = torch.arange(case["rows"], device="cuda")[targets >= 0], targets[targets >= 0]
+    entropy = -torch.where(p > 0, p * lp, 0.0).sum(1)
+    if op == "token_logprobs":
+        logprob = torch.zeros_like(lse)
+        logprob[hit[0]] = lp[hit]
+        out = {"logprob": logprob, "lse": lse, "entropy": entropy}
+        if case["top"]:
+            v, i = torch.sort(x, dim=1, descending=True, stable=True)
+            out |= {"top_ids": i[:, :case["top"]].contiguous(), "top_logprob": v[:, :case["top"]] - lse[:, None]}
+        return out
+    # of the exact statistics, where the plain form takes the forward pass's
+    g, gh = state["g"].double(), state["gh"].double()
+    dx = -gh[:, None] * torch.where(p > 0, p * (lp + entropy[:, None]), 0.0)
+    one = torch.zeros_like(x)
+    one[hit] = 1.0
+    return dx + torch.where(targets >= 0, g, 0.0)[:, None] * (one - p)
