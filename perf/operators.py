@@ -71,7 +71,7 @@ def draw(rng):
         groups = max(1, min(groups, (1 << 30) // (n * k)))
         rows = _spread(rng, 1, min(16384, 2 ** 39 // (n * k)))
         return {"op": op, "rows": rows, "n": n, "k": k, "groups": groups, "skew": round(rng.uniform(0, 1.5), 2),
-                "scale": rng.choice(["row", "block"]), "out": rng.choice(["bf16", "bf16", "f32", "f16"])}
+                "scale": rng.choice(["row", "block"]), "out": rng.choice(["bf16", "bf16", "f16"])}
     groups = max(1, min(_spread(rng, 2, 64), (1 << 28) // (n * k)))
     rows = _spread(rng, 1, min(16384, 2 ** 38 // (n * k)))
     return {"op": op, "rows": rows, "n": n, "k": k, "groups": groups, "skew": round(rng.uniform(0, 1.5), 2),
