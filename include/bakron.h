@@ -53,6 +53,7 @@ extern "C" {
 #define BAKRON_DEV_NONFINITE 1  /* a non-finite weight or error term was met */
 #define BAKRON_DEV_NOT_PD 2     /* a non-positive pivot in bakron_factor */
 #define BAKRON_DEV_SPIN_LIMIT 4 /* a bounded wait inside a kernel gave up (results invalid) */
+#define BAKRON_DEV_BAD_INDEX 8  /* a target or a group offset out of range */
 
 /* base quantizer kinds (the solver is modular in the base quantizer; review
  * page abstract).  Per-row (output channel) parameters from the ORIGINAL W:
@@ -266,6 +267,136 @@ int32_t bakron_schedule_plan(int64_t m, int64_t n, int32_t flags, int32_t *ops, 
  * gaps; the replays rewrite the workspace, not the outputs).  Returns
  * BAKRON_ERR_INVALID_ARG if no such call was made. */
 int32_t bakron_last_phase_ms(double *out);
+
+/* ---------------------------------------------------------------------------
+ * Operators for rounded layers: what multiplies with the solver's result, by
+ * expert where a layer has experts, and what says how a model's answers moved.
+ * For these calls a matrix's rows may be `ld` elements apart (ld >= its width;
+ * any ld and any alignment of one element are accepted, rows that begin on 16
+ * bytes are faster).  Sizes are limited to 2^24 unless noted.
+ */
+
+/* element types */
+#define BAKRON_T_F32 0
+#define BAKRON_T_BF16 1
+#define BAKRON_T_F16 2
+
+/*
+ * bakron_fp8_quantize -- X in 8-bit floating point (e4m3: 3 mantissa bits,
+ * largest value 448) with a scale for each row and 128 columns (block_rows 1:
+ * activations) or each 128 x 128 block (block_rows 128: weights); the blocks at
+ * the right and lower edge may be smaller.
+ *   amax = max |x| of the block, at least 2^-100;  scale = amax / 448 (1 for a
+ *   block of zeros);  Q = e4m3(clamp(x (448 / amax), -448, 448)), to nearest even
+ *   X       rows x cols, `type` BAKRON_T_*, row stride ldx.  rows, cols <= 2^22.
+ *   Q       rows x cols codes, row stride ldq.
+ *   scales  ceil(cols / 128) x ceil(rows / block_rows), contiguous: the scales
+ *           of one block of columns lie together, as the product reads them.
+ * A block that holds a NaN or an infinity gets NaN codes and a NaN scale, and
+ * sets BAKRON_DEV_NONFINITE in *dev_status (may be NULL).
+ */
+int32_t bakron_fp8_quantize(const void *X, int32_t type, int64_t rows, int64_t cols, int64_t ldx,
+                            int32_t block_rows, uint8_t *Q, int64_t ldq, float *scales,
+                            int32_t *dev_status, void *stream);
+
+/*
+ * bakron_fp8_from_codes -- a solve's codes as e4m3 weights, exactly: Q = c - z,
+ * an integer in [-15, 15] for every kind and width accepted here (BAKRON_Q_SYM
+ * and BAKRON_Q_ASYM with 2 to 4 bits).  With the solve's row scales,
+ * bakron_fp8_matmul (BAKRON_SCALE_ROW) multiplies with V itself.
+ *   codes  m x n (contiguous, as bakron_quantize writes them)
+ *   zeros  m zero points for BAKRON_Q_ASYM, else NULL
+ *   Q      m x n, row stride ldq
+ */
+int32_t bakron_fp8_from_codes(const int8_t *codes, const float *zeros, int64_t m, int64_t n, int32_t qkind,
+                              int32_t qbits, uint8_t *Q, int64_t ldq, void *stream);
+
+/* scales of fp8 weights */
+#define BAKRON_SCALE_ROW 0   /* one for each row */
+#define BAKRON_SCALE_BLOCK 1 /* one for each 128 x 128 block */
+
+/*
+ * Rows by group.  `offsets` (device, groups + 1 values, from 0 on, not falling,
+ * the last at most rows) gives group g the rows offsets[g] .. offsets[g+1] - 1
+ * of X and Y; groups may be empty.  Rows after the last group's get 0.  Offsets
+ * that fall or leave [0, rows] set BAKRON_DEV_BAD_INDEX in *dev_status; nothing
+ * outside the matrices is touched, and the result is undefined.  `offsets` NULL
+ * goes with groups = 1: all rows.  The host never reads offsets.
+ * Products are summed on the matrix cores in fp32; the order is fixed, so equal
+ * inputs give equal bits.
+ *
+ * bakron_fp8_matmul -- Y = X W_g^T, both operands in e4m3 with scales:
+ *   Y[r][n] = sum_b sx[b][r] sw(g, b, n) sum_{k in block b} X[r][k] W_g[n][k]
+ * over blocks b of 128 of k.
+ *   X   rows x K codes, row stride ldx;   sx  ceil(K / 128) x rows
+ *   W   groups x N x K codes, row stride ldw, groups N ldw apart
+ *   sw  wscale BAKRON_SCALE_ROW:   groups x N
+ *       wscale BAKRON_SCALE_BLOCK: groups x ceil(K / 128) x ceil(N / 128)
+ *   Y   rows x N in ytype (bf16 or fp16; the fp8 matrix cores keep too few bits
+ *       of a sum for an fp32 result), row stride ldy
+ *   ws  bakron_fp8_matmul_workspace_size() bytes
+ */
+size_t bakron_fp8_matmul_workspace_size(int64_t rows, int64_t N, int64_t K, int32_t groups);
+int32_t bakron_fp8_matmul(const uint8_t *X, int64_t ldx, const float *sx, const uint8_t *W, int64_t ldw,
+                          const float *sw, int32_t wscale, int64_t rows, int64_t N, int64_t K,
+                          int32_t groups, const int32_t *offsets, void *Y, int32_t ytype, int64_t ldy,
+                          int32_t *dev_status, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * bakron_grouped_matmul -- Y[r] = X[r] W_g(r)^T, and its gradients
+ *   grad_x:  dX[r] = dY[r] W_g(r)        grad_w:  dW_g = dY_g^T X_g (0 for an empty group)
+ *   X, dX rows x K;  W, dW groups x N x K (groups N ldw apart);  Y, dY rows x N
+ * Inputs are bf16 or fp16 (`type`); the output is of that type or fp32.
+ *   ws  *_workspace_size() bytes
+ */
+size_t bakron_grouped_matmul_workspace_size(int64_t rows, int64_t N, int64_t K, int32_t groups);
+int32_t bakron_grouped_matmul(const void *X, int32_t type, int64_t ldx, const void *W, int64_t ldw,
+                              int64_t rows, int64_t N, int64_t K, int32_t groups, const int32_t *offsets,
+                              void *Y, int32_t ytype, int64_t ldy, int32_t *dev_status, void *ws,
+                              size_t ws_bytes, void *stream);
+int32_t bakron_grouped_matmul_grad_x(const void *dY, int32_t type, int64_t lddy, const void *W, int64_t ldw,
+                                     int64_t rows, int64_t N, int64_t K, int32_t groups,
+                                     const int32_t *offsets, void *dX, int32_t dxtype, int64_t lddx,
+                                     int32_t *dev_status, void *ws, size_t ws_bytes, void *stream);
+int32_t bakron_grouped_matmul_grad_w(const void *dY, int32_t type, int64_t lddy, const void *X, int64_t ldx,
+                                     int64_t rows, int64_t N, int64_t K, int32_t groups,
+                                     const int32_t *offsets, void *dW, int32_t dwtype, int64_t lddw,
+                                     int32_t *dev_status, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * bakron_token_logprobs -- log probabilities of given tokens, with entropy and
+ * the k likeliest tokens.  Per row of logits x:
+ *   lse = log sum_j e^x_j;  logprob = x_target - lse;  entropy = -sum_j p_j log p_j
+ *   top: the k largest log probabilities and their tokens, in falling order,
+ *        equal values by lowest index.
+ *   logits   rows x vocab, `type` BAKRON_T_*, row stride ld.  -inf masks a token.
+ *            vocab <= 2^21, k <= min(64, vocab).
+ *   targets  rows token numbers; a negative one gives logprob 0.  One >= vocab
+ *            gives NaN and sets BAKRON_DEV_BAD_INDEX.
+ *   logprob, lse, entropy  rows fp32.   top_logprob, top_ids  rows x k (k > 0).
+ * A row of -inf only has no distribution: lse = logprob = top_logprob = -inf,
+ * entropy 0.  A row with a NaN or +inf gives NaN and sets BAKRON_DEV_NONFINITE
+ * (its top_ids are tokens of the row, in no order that is defined).
+ */
+size_t bakron_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int32_t k);
+int32_t bakron_token_logprobs(const void *logits, int32_t type, int64_t rows, int64_t vocab, int64_t ld,
+                              const int64_t *targets, int32_t k, float *logprob, float *lse, float *entropy,
+                              float *top_logprob, int64_t *top_ids, int32_t *dev_status, void *ws,
+                              size_t ws_bytes, void *stream);
+
+/*
+ * bakron_token_logprobs_grad -- the gradient of sum_r (g_logprob logprob +
+ * g_entropy entropy) with respect to the logits:
+ *   dlogits_j = g_logprob ([j = target] - p_j) - g_entropy p_j (log p_j + entropy)
+ * from the forward call's lse and entropy.  Rows without a target have no first
+ * term, rows of -inf only get 0.  g_entropy may be NULL (then entropy may be).
+ * dlogits has the logits' type, row stride ldd.  With g_logprob = 1 its rows are
+ * the last layer's output-side samples (bakron_hessian).
+ */
+int32_t bakron_token_logprobs_grad(const void *logits, int32_t type, int64_t rows, int64_t vocab, int64_t ld,
+                                   const int64_t *targets, const float *lse, const float *entropy,
+                                   const float *g_logprob, const float *g_entropy, void *dlogits,
+                                   int64_t ldd, int32_t *dev_status, void *stream);
 
 const char *bakron_status_string(int32_t status);
 const char *bakron_last_error(void);

@@ -23,6 +23,9 @@ FLAG_MSE_SCALE = 16
 FLAG_SPLIT_COLS = 32
 FLAG_SPLIT_ROWS = 64
 DEV_NONFINITE, DEV_NOT_PD = 1, 2
+DEV_BAD_INDEX = 8
+T_F32, T_BF16, T_F16 = 0, 1, 2
+SCALE_ROW, SCALE_BLOCK = 0, 1
 
 EXPORTS = (
     "bakron_hessian_workspace_size", "bakron_hessian",
@@ -30,6 +33,11 @@ EXPORTS = (
     "bakron_quantize_workspace_size", "bakron_quantize", "bakron_quantize_noalloc",
     "bakron_quantize_antidiag_workspace_size", "bakron_quantize_antidiag",
     "bakron_schedule_info", "bakron_schedule_plan", "bakron_last_phase_ms",
+    "bakron_fp8_quantize", "bakron_fp8_from_codes",
+    "bakron_fp8_matmul_workspace_size", "bakron_fp8_matmul",
+    "bakron_grouped_matmul_workspace_size", "bakron_grouped_matmul", "bakron_grouped_matmul_grad_x",
+    "bakron_grouped_matmul_grad_w",
+    "bakron_token_logprobs_workspace_size", "bakron_token_logprobs", "bakron_token_logprobs_grad",
     "bakron_status_string", "bakron_last_error",
 )
 
@@ -75,6 +83,26 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.bakron_schedule_plan.restype = I32
     lib.bakron_last_phase_ms.argtypes = [ctypes.POINTER(D)]
     lib.bakron_last_phase_ms.restype = I32
+    lib.bakron_fp8_quantize.argtypes = [P, I32, I64, I64, I64, I32, P, I64, P, P, P]
+    lib.bakron_fp8_quantize.restype = I32
+    lib.bakron_fp8_from_codes.argtypes = [P, P, I64, I64, I32, I32, P, I64, P]
+    lib.bakron_fp8_from_codes.restype = I32
+    lib.bakron_fp8_matmul_workspace_size.argtypes = [I64, I64, I64, I32]
+    lib.bakron_fp8_matmul_workspace_size.restype = SZ
+    lib.bakron_fp8_matmul.argtypes = [P, I64, P, P, I64, P, I32, I64, I64, I64, I32, P, P, I32, I64, P, P,
+                                      SZ, P]
+    lib.bakron_fp8_matmul.restype = I32
+    lib.bakron_grouped_matmul_workspace_size.argtypes = [I64, I64, I64, I32]
+    lib.bakron_grouped_matmul_workspace_size.restype = SZ
+    for f in (lib.bakron_grouped_matmul, lib.bakron_grouped_matmul_grad_x, lib.bakron_grouped_matmul_grad_w):
+        f.argtypes = [P, I32, I64, P, I64, I64, I64, I64, I32, P, P, I32, I64, P, P, SZ, P]
+        f.restype = I32
+    lib.bakron_token_logprobs_workspace_size.argtypes = [I64, I64, I32]
+    lib.bakron_token_logprobs_workspace_size.restype = SZ
+    lib.bakron_token_logprobs.argtypes = [P, I32, I64, I64, I64, P, I32, P, P, P, P, P, P, P, SZ, P]
+    lib.bakron_token_logprobs.restype = I32
+    lib.bakron_token_logprobs_grad.argtypes = [P, I32, I64, I64, I64, P, P, P, P, P, P, I64, P, P]
+    lib.bakron_token_logprobs_grad.restype = I32
     lib.bakron_status_string.argtypes = [I32]
     lib.bakron_status_string.restype = ctypes.c_char_p
     lib.bakron_last_error.argtypes = []
@@ -274,3 +302,230 @@ def last_phase_ms() -> dict:
     buf = (ctypes.c_double * len(PHASE_KEYS))()
     _check(lib.bakron_last_phase_ms(buf), "bakron_last_phase_ms")
     return dict(zip(PHASE_KEYS, list(buf)))
+
+
+# Operators for rounded layers.  Matrices are GPU tensors whose rows may lie apart
+# (a row's elements are adjacent); nothing is copied to make them contiguous.
+
+_TYPES = {torch.float32: T_F32, torch.bfloat16: T_BF16, torch.float16: T_F16}
+_FP8 = torch.float8_e4m3fn
+
+
+def _rows_of(t, name, dtypes, ndim=2):
+    """The element distance between t's rows, after the checks that every matrix gets."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise BakronError(f"{name} must be on the current GPU")
+    if t.dtype not in dtypes:
+        raise BakronError(f"{name} must be one of {[str(d) for d in dtypes]}, not {t.dtype}")
+    if t.dim() != ndim or t.numel() == 0:
+        raise BakronError(f"{name} must have {ndim} dimensions, none of size 0, not {tuple(t.shape)}")
+    *lead, last = t.stride()
+    if last != 1 and t.shape[-1] != 1:
+        raise BakronError(f"the elements of a row of {name} must be adjacent")
+    ld = lead[-1] if t.shape[-2] != 1 else max(lead[-1], t.shape[-1])
+    if ndim == 3 and t.shape[0] != 1 and lead[0] != t.shape[1] * ld:
+        raise BakronError(f"the matrices of {name} must lie {t.shape[1]} rows apart")
+    return ld
+
+
+def _vector(t, name, dtype, shape):
+    """t's pointer if it is a contiguous GPU tensor of this dtype and shape."""
+    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise BakronError(f"{name} must be a contiguous {dtype} GPU tensor of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _out(out, shape, dtype, device, name):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype:
+        raise BakronError(f"{name} must be {dtype} of shape {tuple(shape)}")
+    return out
+
+
+def _where(stream, *tensors):
+    """The stream's handle.  What this module allocated and hands to a stream other
+    than torch's current one is marked as used there."""
+    current = torch.cuda.current_stream()
+    if stream is None or stream.cuda_stream == current.cuda_stream:
+        return current.cuda_stream
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _status(t):
+    return None if t is None else _vector(t, "dev_status", torch.int32, (1,))
+
+
+def fp8_quantize(X, block_rows=1, out=None, scales=None, dev_status=None, stream=None):
+    """X in e4m3 with a scale for each row (block_rows 1) or 128 rows (128) and 128
+    columns (bakron_fp8_quantize).  Returns (codes as float8_e4m3fn, scales of
+    shape (ceil(cols / 128), ceil(rows / block_rows)))."""
+    lib = load()
+    ldx = _rows_of(X, "X", _TYPES)
+    rows, cols = X.shape
+    if block_rows not in (1, 128):
+        raise BakronError(f"block_rows must be 1 or 128, not {block_rows}")
+    Q = _out(out, (rows, cols), _FP8, X.device, "out")
+    ldq = _rows_of(Q, "out", (_FP8,))
+    S = _out(scales, (-(-cols // 128), -(-rows // block_rows)), torch.float32, X.device, "scales")
+    sp = _vector(S, "scales", torch.float32, S.shape)
+    _check(lib.bakron_fp8_quantize(X.data_ptr(), _TYPES[X.dtype], rows, cols, ldx, block_rows, Q.data_ptr(),
+                                   ldq, sp, _status(dev_status), _where(stream, Q, S)), "bakron_fp8_quantize")
+    return Q, S
+
+
+def fp8_from_codes(codes, zeros=None, kind=Q_SYM, bits=4, out=None, stream=None):
+    """The codes of a solve (2 to 4 bits) as e4m3 weights, exactly (bakron_fp8_from_codes)."""
+    lib = load()
+    if codes.dim() != 2 or codes.numel() == 0:
+        raise BakronError(f"codes must have 2 dimensions, none of size 0, not {tuple(codes.shape)}")
+    m, n = codes.shape
+    cp = _vector(codes, "codes", torch.int8, (m, n))
+    zp = None if zeros is None else _vector(zeros, "zeros", torch.float32, (m,))
+    Q = _out(out, (m, n), _FP8, codes.device, "out")
+    ldq = _rows_of(Q, "out", (_FP8,))
+    _check(lib.bakron_fp8_from_codes(cp, zp, m, n, kind, bits, Q.data_ptr(), ldq, _where(stream, Q)),
+           "bakron_fp8_from_codes")
+    return Q
+
+
+def _groups(W, offsets):
+    groups = W.shape[0] if W.dim() == 3 else 1
+    if offsets is None:
+        if groups != 1:
+            raise BakronError("offsets are needed where W has groups")
+        return groups, None
+    return groups, _vector(offsets, "offsets", torch.int32, (groups + 1,))
+
+
+def _space(nbytes, device):
+    """A workspace of nbytes, or None for none."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def fp8_matmul(X, sx, W, sw, offsets=None, out_dtype=torch.bfloat16, out=None, dev_status=None, stream=None):
+    """Y = X W^T of e4m3 operands with scales (bakron_fp8_matmul).
+
+    X (rows, K) with sx (ceil(K / 128), rows); W (N, K), or (groups, N, K) with
+    offsets (int32, groups + 1, on the GPU).  sw has one scale for each row of W,
+    of shape (N,) or (groups, N), or one for each block, of shape (ceil(K / 128),
+    ceil(N / 128)) or (groups, ...).  out_dtype: bfloat16 or float16."""
+    lib = load()
+    ldx = _rows_of(X, "X", (_FP8,))
+    ldw = _rows_of(W, "W", (_FP8,), 3 if W.dim() == 3 else 2)
+    rows, K = X.shape
+    N = W.shape[-2]
+    if W.shape[-1] != K:
+        raise BakronError(f"W's rows have {W.shape[-1]} elements, X's {K}")
+    groups, op = _groups(W, offsets)
+    kb, lead = -(-K // 128), tuple(W.shape[:-2])
+    sxp = _vector(sx, "sx", torch.float32, (kb, rows))
+    if sw.dim() == W.dim():
+        wscale, swp = SCALE_BLOCK, _vector(sw, "sw", torch.float32, (*lead, kb, -(-N // 128)))
+    else:
+        wscale, swp = SCALE_ROW, _vector(sw, "sw", torch.float32, (*lead, N))
+    if out_dtype not in (torch.bfloat16, torch.float16):
+        raise BakronError(f"out_dtype must be bfloat16 or float16, not {out_dtype}")
+    Y = _out(out, (rows, N), out_dtype, X.device, "out")
+    ldy = _rows_of(Y, "out", _TYPES)
+    ws = _space(lib.bakron_fp8_matmul_workspace_size(rows, N, K, groups), X.device)
+    _check(lib.bakron_fp8_matmul(X.data_ptr(), ldx, sxp, W.data_ptr(), ldw, swp, wscale, rows, N, K, groups,
+                                 op, Y.data_ptr(), _TYPES[out_dtype], ldy, _status(dev_status),
+                                 None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                                 _where(stream, Y, ws)), "bakron_fp8_matmul")
+    return Y
+
+
+def _grouped(fn, what, A, B, rows, N, K, groups, op, shape, out_dtype, out, dev_status, stream):
+    lib = load()
+    lda = _rows_of(A, "the left operand", (torch.bfloat16, torch.float16))
+    ldb = _rows_of(B, "the right operand", (A.dtype,), B.dim())
+    dtype = A.dtype if out_dtype is None else out_dtype
+    if dtype not in (A.dtype, torch.float32):
+        raise BakronError(f"the output's dtype must be {A.dtype} or float32, not {dtype}")
+    Y = _out(out, shape, dtype, A.device, "out")
+    ldy = _rows_of(Y, "out", (dtype,), len(shape))
+    ws = _space(lib.bakron_grouped_matmul_workspace_size(rows, N, K, groups), A.device)
+    _check(fn(A.data_ptr(), _TYPES[A.dtype], lda, B.data_ptr(), ldb, rows, N, K, groups, op, Y.data_ptr(),
+              _TYPES[dtype], ldy, _status(dev_status), None if ws is None else ws.data_ptr(),
+              0 if ws is None else ws.numel(), _where(stream, Y, ws)), what)
+    return Y
+
+
+def grouped_matmul(X, W, offsets=None, out_dtype=None, out=None, dev_status=None, stream=None):
+    """Y[r] = X[r] W_g(r)^T (bakron_grouped_matmul).  X (rows, K) and W (groups, N, K)
+    in bfloat16 or float16, offsets (int32, groups + 1, on the GPU): group g has the
+    rows offsets[g] .. offsets[g + 1] - 1.  out_dtype: X's (the default) or float32."""
+    groups, op = _groups(W, offsets)
+    if X.dim() != 2 or W.dim() not in (2, 3) or W.shape[-1] != X.shape[1]:
+        raise BakronError(f"X {tuple(X.shape)} and W {tuple(W.shape)} do not fit")
+    rows, K, N = X.shape[0], X.shape[1], W.shape[-2]
+    return _grouped(load().bakron_grouped_matmul, "bakron_grouped_matmul", X, W, rows, N, K, groups, op,
+                    (rows, N), out_dtype, out, dev_status, stream)
+
+
+def grouped_matmul_grad(dY, X, W, offsets=None, want_x=True, want_w=True, w_dtype=None, dev_status=None,
+                        stream=None):
+    """grouped_matmul's gradients (dX, dW) for dY (bakron_grouped_matmul_grad_x and
+    _grad_w).  One that is not wanted is None.  w_dtype: X's (the default) or float32."""
+    groups, op = _groups(W, offsets)
+    if X.dim() != 2 or W.dim() not in (2, 3) or W.shape[-1] != X.shape[1] or \
+            tuple(dY.shape) != (X.shape[0], W.shape[-2]):
+        raise BakronError(f"dY {tuple(dY.shape)}, X {tuple(X.shape)} and W {tuple(W.shape)} do not fit")
+    rows, K, N = X.shape[0], X.shape[1], W.shape[-2]
+    lib, dX, dW = load(), None, None
+    if want_x:
+        dX = _grouped(lib.bakron_grouped_matmul_grad_x, "bakron_grouped_matmul_grad_x", dY, W, rows, N, K,
+                      groups, op, (rows, K), None, None, dev_status, stream)
+    if want_w:
+        dW = _grouped(lib.bakron_grouped_matmul_grad_w, "bakron_grouped_matmul_grad_w", dY, X, rows, N, K,
+                      groups, op, tuple(W.shape), w_dtype, None, dev_status, stream)
+    return dX, dW
+
+
+def token_logprobs(logits, targets, top=0, dev_status=None, stream=None):
+    """Log probabilities of the targets (int64, negative: none), with entropy and the
+    `top` likeliest tokens (bakron_token_logprobs).  Returns a dict with logprob,
+    lse, entropy (rows) and top_logprob, top_ids (rows, top; None for top 0)."""
+    lib = load()
+    ld = _rows_of(logits, "logits", _TYPES)
+    rows, vocab = logits.shape
+    tp = _vector(targets, "targets", torch.int64, (rows,))
+    if not 0 <= top <= min(64, vocab):
+        raise BakronError(f"top must be in 0 .. {min(64, vocab)}, not {top}")
+    dev = logits.device
+    stats = torch.empty((3, rows), dtype=torch.float32, device=dev)
+    tl = torch.empty((rows, top), dtype=torch.float32, device=dev) if top else None
+    ti = torch.empty((rows, top), dtype=torch.int64, device=dev) if top else None
+    ws = _space(lib.bakron_token_logprobs_workspace_size(rows, vocab, top), dev)
+    sp = stats.data_ptr()
+    _check(lib.bakron_token_logprobs(logits.data_ptr(), _TYPES[logits.dtype], rows, vocab, ld, tp, top, sp,
+                                     sp + 4 * rows, sp + 8 * rows, tl.data_ptr() if top else None,
+                                     ti.data_ptr() if top else None, _status(dev_status),
+                                     None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                                     _where(stream, stats, tl, ti, ws)), "bakron_token_logprobs")
+    return dict(logprob=stats[0], lse=stats[1], entropy=stats[2], top_logprob=tl, top_ids=ti)
+
+
+def token_logprobs_grad(logits, targets, lse, entropy, g_logprob, g_entropy=None, out=None, dev_status=None,
+                        stream=None):
+    """The gradient of sum(g_logprob logprob + g_entropy entropy) with respect to the
+    logits (bakron_token_logprobs_grad), from the forward call's lse and entropy."""
+    lib = load()
+    ld = _rows_of(logits, "logits", _TYPES)
+    rows, vocab = logits.shape
+    f32 = torch.float32
+    D = _out(out, (rows, vocab), logits.dtype, logits.device, "out")
+    ldd = _rows_of(D, "out", (logits.dtype,))
+    if g_entropy is not None and entropy is None:
+        raise BakronError("g_entropy needs the forward call's entropy")
+    _check(lib.bakron_token_logprobs_grad(
+        logits.data_ptr(), _TYPES[logits.dtype], rows, vocab, ld, _vector(targets, "targets", torch.int64, (rows,)),
+        _vector(lse, "lse", f32, (rows,)), None if entropy is None else _vector(entropy, "entropy", f32, (rows,)),
+        _vector(g_logprob, "g_logprob", f32, (rows,)),
+        None if g_entropy is None else _vector(g_entropy, "g_entropy", f32, (rows,)), D.data_ptr(), ldd,
+        _status(dev_status), _where(stream, D)), "bakron_token_logprobs_grad")
+    return D

@@ -14,7 +14,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbakron.so")
 
-SOURCES = ["common.hip", "quantize.hip", "hessian.hip", "factor.hip"]
+SOURCES = ["common.hip", "quantize.hip", "hessian.hip", "factor.hip", "fp8.hip", "products.hip",
+           "logprobs.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
@@ -39,7 +40,8 @@ def hipcc() -> str:
 def build(verbose: bool = False) -> str:
     srcs = [os.path.join(CSRC, s) for s in SOURCES if os.path.exists(os.path.join(CSRC, s))]
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, *srcs, "-o", tmp]
+    # the sources compile side by side
+    cmd = [hipcc(), *HIPCC_FLAGS, "-parallel-jobs=8", "-I", INCLUDE, "-I", CSRC, *srcs, "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
