@@ -72,6 +72,13 @@ def test_fp8_matmul(lib):
     refused(lib, call(ldy=63), b"ldy")
     refused(lib, call(yt=0), b"type")
     refused(lib, call(Y=ODD), b"misaligned")
+    need = lib.bakron_fp8_matmul_workspace_size(64, 64, 8192, 1)
+    assert need > 0 and lib.bakron_fp8_matmul_workspace_size(0, 64, 64, 1) == 0
+    def small(ws, size):
+        return lib.bakron_fp8_matmul(F, 8192, F, F, 8192, F, 0, 64, 64, 8192, 1, None, F, 1, 64, None, ws, size, None)
+    refused(lib, small(F, 4096), b"workspace", 2)
+    refused(lib, small(None, need), b"workspace", 2)
+    refused(lib, small(ctypes.c_void_p(4096 + 8), need), b"workspace", 2)
 
 
 @pytest.mark.parametrize("name", ["bakron_grouped_matmul", "bakron_grouped_matmul_grad_x",

@@ -157,7 +157,26 @@ FP8_CASES = [
     (65, 257, 513, 1, "row", "bf16", 0), (128, 128, 1024, 1, "block", "bf16", 0), (300, 1000, 400, 1, "block", "f16", 0),
     (515, 520, 528, 1, "row", "bf16", 16), (1, 1024, 4096, 1, "row", "bf16", 0), (1025, 1032, 272, 1, "block", "bf16", 0),
     (40, 96, 160, 8, "row", "bf16", 0), (333, 200, 144, 7, "block", "bf16", 0), (1000, 384, 512, 70, "row", "f16", 0),
-    (64, 130, 77, 5, "block", "bf16", 3), (2500, 300, 256, 3, "row", "bf16", 0), (4200, 1100, 640, 2, "block", "bf16", 0)]
+    (64, 130, 77, 5, "block", "bf16", 3), (2500, 300, 256, 3, "row", "bf16", 0), (4200, 1100, 640, 2, "block", "bf16", 0),
+    # enough tiles for the large ones
+    (4100, 2120, 656, 3, "row", "bf16", 0), (4100, 2120, 912, 1, "block", "f16", 16), (4100, 2125, 144, 1, "block", "bf16", 0),
+    # few rows: the form for single tokens, its widths and ends
+    (1, 4096, 1040, 1, "block", "bf16", 0), (2, 40, 2500, 1, "row", "f16", 1), (20, 1000, 384, 1, "block", "bf16", 0),
+    (50, 333, 640, 1, "row", "bf16", 0), (64, 512, 129, 1, "block", "f16", 0), (30, 272, 400, 16, "row", "bf16", 0),
+    (150, 100, 256, 9, "block", "bf16", 0),
+    # few tiles and a long reduction, which is split
+    (40, 260, 4200, 1, "block", "bf16", 0), (130, 100, 6416, 1, "row", "f16", 0), (200, 130, 4112, 3, "block", "bf16", 0)]
+SPLIT_CASES = [(40, 260, 4200, 1), (130, 100, 6416, 1), (200, 130, 4112, 3)]
+
+
+def test_long_reductions_are_split(bk):
+    """The cases above that stand for split reductions have a workspace, the others' sizes none."""
+    for rows, n, k, groups in SPLIT_CASES:
+        assert bk.load().bakron_fp8_matmul_workspace_size(rows, n, k, groups) > 0
+    for rows, n, k, groups in ((300, 136, 2104, 3), (100, 2201, 130, 2), (6000, 130, 70, 2), (5000, 136, 72, 3)):
+        assert bk.load().bakron_grouped_matmul_workspace_size(rows, n, k, groups) > 0
+    assert bk.load().bakron_fp8_matmul_workspace_size(1, 4096, 4096, 1) == 0
+    assert bk.load().bakron_fp8_matmul_workspace_size(8192, 4096, 4096, 1) == 0
 
 
 @pytest.mark.parametrize("rows,n,k,groups,scale,out,pad", FP8_CASES)
@@ -199,7 +218,16 @@ GROUPED_CASES = [
     (37, 130, 70, 5, "f16", "f32", 1, 1), (64, 256, 128, 64, "bf16", None, 0, 0), (100, 72, 200, 9, "bf16", None, 8, 8),
     (257, 264, 136, 2, "f16", None, 0, 0), (300, 520, 520, 24, "f16", None, 0, 0), (513, 128, 1000, 3, "bf16", "f32", 0, 0),
     (1000, 384, 256, 130, "bf16", None, 0, 0), (1500, 1000, 328, 4, "bf16", None, 0, 0), (2050, 301, 259, 3, "f16", None, 0, 0),
-    (4300, 560, 328, 3, "bf16", "f32", 8, 0)]
+    (4300, 560, 328, 3, "bf16", "f32", 8, 0),
+    # enough tiles for the large ones: forward, gradient of X, gradient of W
+    (4100, 2120, 328, 3, "bf16", None, 0, 0), (4100, 328, 2120, 2, "f16", "f32", 8, 8), (700, 2056, 1416, 3, "bf16", None, 0, 0),
+    (4100, 2128, 264, 1, "f16", "f32", 0, 0),
+    # few rows
+    (1, 300, 1000, 1, "bf16", None, 0, 0), (2, 33, 2050, 1, "f16", "f32", 1, 1), (60, 1000, 200, 1, "bf16", None, 0, 0),
+    (90, 130, 520, 7, "bf16", "f32", 0, 0), (33, 272, 264, 40, "f16", None, 0, 0),
+    # few tiles and a long reduction, which is split: forward, gradients
+    (300, 136, 2104, 3, "bf16", None, 0, 0), (100, 2201, 130, 2, "f16", "f32", 0, 0), (6000, 130, 70, 2, "bf16", "f32", 0, 0),
+    (5000, 136, 72, 3, "f16", None, 0, 0)]
 
 
 def product_inputs(rows, n, k, groups, dtype, seed):

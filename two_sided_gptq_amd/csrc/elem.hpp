@@ -78,10 +78,14 @@ __device__ __forceinline__ void load8(const char *base, int64_t i, int64_t left,
 // Bit pattern of 2 values in a 16-bit type, low half first.
 template <int T>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
+    typedef float floatx2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    const floatx2 v = {a, b};
     if constexpr (T == BAKRON_T_BF16)
-        return (uint32_t)f32_to_bf16(a) | ((uint32_t)f32_to_bf16(b) << 16);
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
     else
-        return (uint32_t)f32_to_f16(a) | ((uint32_t)f32_to_f16(b) << 16);
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
 }
 
 template <int T>
