@@ -313,24 +313,25 @@ _FP8 = torch.float8_e4m3fn
 
 def _rows_of(t, name, dtypes, ndim=2):
     """The element distance between t's rows, after the checks that every matrix gets."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    shape, stride, dev = t.shape, t.stride(), t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise BakronError(f"{name} must be on the current GPU")
     if t.dtype not in dtypes:
         raise BakronError(f"{name} must be one of {[str(d) for d in dtypes]}, not {t.dtype}")
-    if t.dim() != ndim or t.numel() == 0:
-        raise BakronError(f"{name} must have {ndim} dimensions, none of size 0, not {tuple(t.shape)}")
-    *lead, last = t.stride()
-    if last != 1 and t.shape[-1] != 1:
+    if len(shape) != ndim or 0 in shape:
+        raise BakronError(f"{name} must have {ndim} dimensions, none of size 0, not {tuple(shape)}")
+    n, k = shape[-2], shape[-1]
+    if k != 1 and stride[-1] != 1:
         raise BakronError(f"the elements of a row of {name} must be adjacent")
-    ld = lead[-1] if t.shape[-2] != 1 else max(lead[-1], t.shape[-1])
-    if ndim == 3 and t.shape[0] != 1 and lead[0] != t.shape[1] * ld:
-        raise BakronError(f"the matrices of {name} must lie {t.shape[1]} rows apart")
+    ld = stride[-2] if n != 1 else max(stride[-2], k)
+    if ndim == 3 and shape[0] != 1 and stride[0] != n * ld:
+        raise BakronError(f"the matrices of {name} must lie {n} rows apart")
     return ld
 
 
 def _vector(t, name, dtype, shape):
     """t's pointer if it is a contiguous GPU tensor of this dtype and shape."""
-    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise BakronError(f"{name} must be a contiguous {dtype} GPU tensor of shape {tuple(shape)}")
     return t.data_ptr()
 
@@ -338,7 +339,7 @@ def _vector(t, name, dtype, shape):
 def _out(out, shape, dtype, device, name):
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != tuple(shape) or out.dtype != dtype:
+    if out.shape != shape or out.dtype != dtype:
         raise BakronError(f"{name} must be {dtype} of shape {tuple(shape)}")
     return out
 
@@ -346,9 +347,9 @@ def _out(out, shape, dtype, device, name):
 def _where(stream, *tensors):
     """The stream's handle.  What this module allocated and hands to a stream other
     than torch's current one is marked as used there."""
-    current = torch.cuda.current_stream()
-    if stream is None or stream.cuda_stream == current.cuda_stream:
-        return current.cuda_stream
+    current = torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if stream is None or stream.cuda_stream == current:
+        return current
     for t in tensors:
         if t is not None:
             t.record_stream(stream)
@@ -498,6 +499,7 @@ def token_logprobs(logits, targets, top=0, dev_status=None, stream=None):
         raise BakronError(f"top must be in 0 .. {min(64, vocab)}, not {top}")
     dev = logits.device
     stats = torch.empty((3, rows), dtype=torch.float32, device=dev)
+    logprob, lse, entropy = stats.unbind()
     tl = torch.empty((rows, top), dtype=torch.float32, device=dev) if top else None
     ti = torch.empty((rows, top), dtype=torch.int64, device=dev) if top else None
     ws = _space(lib.bakron_token_logprobs_workspace_size(rows, vocab, top), dev)
@@ -507,7 +509,7 @@ def token_logprobs(logits, targets, top=0, dev_status=None, stream=None):
                                      ti.data_ptr() if top else None, _status(dev_status),
                                      None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
                                      _where(stream, stats, tl, ti, ws)), "bakron_token_logprobs")
-    return dict(logprob=stats[0], lse=stats[1], entropy=stats[2], top_logprob=tl, top_ids=ti)
+    return dict(logprob=logprob, lse=lse, entropy=entropy, top_logprob=tl, top_ids=ti)
 
 
 def token_logprobs_grad(logits, targets, lse, entropy, g_logprob, g_entropy=None, out=None, dev_status=None,

@@ -7,24 +7,28 @@
 // maximum grows; sums and statistics are fp32.
 //
 // Alternatives (the k largest, equal values by lowest index).  Each thread reads
-// chunks of 16 consecutive elements and leaves each chunk's maximum in LDS.  An
-// element of the k largest lies in one of the k chunks that come first by
-// (maximum, lowest chunk): any other chunk has k chunks before it, each with an
-// element that is larger, or equal at a lower index.  So after the pass only k
-// chunks are read again (from L2).  The selections are by counting: the rank of
-// a key among a short list is the number of keys above it.
+// chunks of consecutive elements and leaves each chunk's maximum.  An element of the k
+// largest lies in one of the k chunks that come first by (maximum, lowest chunk): any
+// other chunk has k chunks before it, each with an element that is larger, or equal at
+// a lower index.  So after the pass only k chunks are read again (from L2).  The
+// selections are by counting: the rank of a key among a short list is the number of
+// keys above it.
+//
+// Many rows: a workgroup takes a row.  Few rows: each is split over workgroups that
+// leave their statistics and chunk maxima in the workspace, and a second launch joins
+// the statistics in a fixed order and selects.
 #include "common.hpp"
 #include "elem.hpp"
 
 namespace bakron {
 namespace {
 
-constexpr int NT = 512;            // threads of a row pass
-constexpr int CE = 16;             // elements of a chunk
-constexpr int SEG_CHUNKS = 8192;   // chunks of a row that one workgroup takes: 32 KB of maxima
-constexpr int64_t SEG = (int64_t)SEG_CHUNKS * CE;
+constexpr int NT = 512;      // threads that take a row, or join one
+constexpr int NTS = 256;     // threads that take a part of a row
+constexpr int CE = 16;       // elements that a thread reads at once
+constexpr int CHUNKS = 8192; // chunks of a row at most: 32 KB of maxima in LDS
 constexpr int KMAX = 64;
-constexpr int CAP = 1024;          // candidates held in LDS
+constexpr int CAP = 1024;    // candidates held in LDS
 
 struct Stats {
     float m, s, t;
@@ -56,12 +60,19 @@ __device__ __forceinline__ float unorder(uint32_t o) {
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t pos) {
     return ((uint64_t)order(x) << 32) | (uint32_t)~pos;
 }
-__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int mask) {
-    const uint32_t lo = (uint32_t)__shfl_xor((int)(uint32_t)v, mask);
-    const uint32_t hi = (uint32_t)__shfl_xor((int)(uint32_t)(v >> 32), mask);
+__device__ __forceinline__ uint64_t max64(uint64_t a, uint64_t b) { return a > b ? a : b; }
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp64(uint64_t v) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, 0xf, 0xf, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, 0xf, 0xf, false);
     return ((uint64_t)hi << 32) | lo;
 }
-__device__ __forceinline__ uint64_t max64(uint64_t a, uint64_t b) { return a > b ? a : b; }
+// The largest of 8 neighbouring lanes, in each of them.
+__device__ __forceinline__ uint64_t max_of_8(uint64_t v) {
+    v = max64(v, dpp64<0xb1>(v));   // quad_perm 1,0,3,2
+    v = max64(v, dpp64<0x4e>(v));   // quad_perm 2,3,0,1
+    return max64(v, dpp64<0x141>(v));  // row_half_mirror: the other four
+}
 
 __device__ __forceinline__ Stats wave_stats(Stats a) {
 #pragma unroll
@@ -75,15 +86,26 @@ __device__ __forceinline__ Stats wave_stats(Stats a) {
     return a;
 }
 
+// How many of list[0, n) are above key; list[n] is 0 and the list 16-byte aligned.
+__device__ __forceinline__ int rank_of(const uint64_t *list, int n, uint64_t key) {
+    int rank = 0;
+#pragma unroll 8
+    for (int j = 0; j < n; j += 2) {
+        const ulong2 two = *reinterpret_cast<const ulong2 *>(list + j);
+        rank += (two.x > key) + (two.y > key);
+    }
+    return rank;
+}
+
 // The k best of list[0, n) (distinct keys, n <= CAP; 0 entries are none) into
 // out[0, k) in order; places without a key get 0.
-__device__ __forceinline__ void rank_select(const uint64_t *list, int n, uint64_t *out, int k) {
+__device__ __forceinline__ void rank_select(uint64_t *list, int n, uint64_t *out, int k) {
     for (int i = threadIdx.x; i < k; i += blockDim.x) out[i] = 0;
+    if (threadIdx.x == 0) list[n] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
         const uint64_t key = list[i];
-        int rank = 0;
-        for (int j = 0; j < n; ++j) rank += list[j] > key;
+        const int rank = rank_of(list, n, key);
         if (rank < k && key) out[rank] = key;
     }
     __syncthreads();
@@ -93,18 +115,31 @@ struct RowArgs {
     const char *x;
     int64_t rows, vocab, ld;
     const int64_t *targets;
-    int k, segs;
-    int64_t seg;  // elements of a segment, a multiple of CE
+    int k, runs;         // a chunk is `runs` times CE elements
+    int chunks;          // of a row
+    int segs, per_seg;   // parts of a row, chunks of a part
     float *logprob, *lse, *entropy, *top_logprob;
     int64_t *top_ids;
     int32_t *dev_status;
-    Stats *part;         // [rows][segs]
-    uint64_t *part_top;  // [rows][segs][k]
+    Stats *part;   // [rows][segs]
+    float *maxima; // [rows][chunks]
 };
 
-// What a row's statistics give; one thread.
+// A row's target and its logit; asked for before the statistics are known, as the two
+// loads depend on each other.
+struct Target {
+    int64_t t;
+    float x;
+};
 template <int T>
-__device__ __forceinline__ float finish_row(const RowArgs &a, int64_t row, Stats st) {
+__device__ __forceinline__ Target target_of(const RowArgs &a, int64_t row) {
+    Target r = {a.targets[row], 0.0f};
+    if (r.t >= 0 && r.t < a.vocab) r.x = load1<T>(a.x, row * a.ld + r.t);
+    return r;
+}
+
+// What a row's statistics give; one thread.
+__device__ __forceinline__ float finish_row(const RowArgs &a, int64_t row, Stats st, Target target) {
     const bool none = st.s == 0.0f;                    // every logit is -inf
     const bool bad = st.s != st.s || st.m > 3.4028235e38f;  // a NaN or +inf
     const float nan = __uint_as_float(0x7fc00000u);
@@ -115,13 +150,12 @@ __device__ __forceinline__ float finish_row(const RowArgs &a, int64_t row, Stats
     int32_t flag = bad ? BAKRON_DEV_NONFINITE : 0;
     a.lse[row] = lse;
     a.entropy[row] = ent;
-    const int64_t t = a.targets[row];
     float lp = 0.0f;
-    if (t >= a.vocab) {
+    if (target.t >= a.vocab) {
         lp = nan;
         flag |= BAKRON_DEV_BAD_INDEX;
-    } else if (t >= 0) {
-        lp = none ? -INFINITY : load1<T>(a.x, row * a.ld + t) - lse;
+    } else if (target.t >= 0) {
+        lp = none ? -INFINITY : target.x - lse;
     }
     a.logprob[row] = lp;
     if (flag && a.dev_status) atomicOr(a.dev_status, flag);
@@ -137,168 +171,197 @@ __device__ __forceinline__ void write_top(const RowArgs &a, int64_t row, const u
     }
 }
 
-// The k best elements of one segment, from its chunks' maxima cmax[0, nchunk).
+// Statistics of a thread's chunks c0 + tid, + threads, .. below c1, with their maxima.
+template <int T, int THREADS>
+__device__ __forceinline__ Stats take_chunks(const RowArgs &a, int64_t base, int c0, int c1, float *maxima) {
+    Stats st = {-3.4028235e38f, 0.0f, 0.0f};
+    for (int c = c0 + threadIdx.x; c < c1; c += THREADS) {
+        float top = -INFINITY;
+        for (int u = 0; u < a.runs; ++u) {
+            const int64_t e = ((int64_t)c * a.runs + u) * CE;
+            float x[CE];
+            if (e + CE <= a.vocab) {
+                load8<T>(a.x, base + e, 8, x);
+                load8<T>(a.x, base + e + 8, 8, x + 8);
+            } else {
+#pragma unroll
+                for (int q = 0; q < CE; ++q) x[q] = e + q < a.vocab ? load1<T>(a.x, base + e + q) : -INFINITY;
+            }
+            float cm = x[0];
+#pragma unroll
+            for (int q = 1; q < CE; ++q) cm = fmaxf(cm, x[q]);
+            top = fmaxf(top, cm);
+            if (cm > st.m) {
+                const float d = st.m - cm, f = __expf(d);
+                st.t = f * (st.t + st.s * fmaxf(d, -200.0f));
+                st.s *= f;
+                st.m = cm;
+            }
+#pragma unroll
+            for (int q = 0; q < CE; ++q) {
+                const float d = x[q] - st.m;  // NaN stays NaN in the sum s
+                const float e1x = __expf(d);
+                st.s += e1x;
+                st.t += e1x * fmaxf(d, -200.0f);  // 0 where e^d vanishes, for d = -inf too
+            }
+        }
+        if (maxima) maxima[c] = top;
+    }
+    return st;
+}
+
+// Statistics of the whole workgroup, in its thread 0.
+template <int THREADS>
+__device__ __forceinline__ Stats block_stats(Stats st, Stats *wave_part) {
+    st = wave_stats(st);
+    if ((threadIdx.x & 63) == 0) wave_part[threadIdx.x >> 6] = st;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        st = wave_part[0];
+        for (int i = 1; i < THREADS / 64; ++i) st = merge(st, wave_part[i]);
+    }
+    return st;
+}
+
+struct TopSpace {
+    float cmax[CHUNKS];
+    __align__(16) uint64_t list[CAP + 2];
+    uint64_t best[KMAX], bound;
+    int count;
+};
+
+// The k best elements of a row into best[0, k), from its chunks' maxima.  NT threads.
 template <int T>
-__device__ void segment_top(const RowArgs &a, int64_t base, int64_t e0, int64_t e1, const float *cmax,
-                            int nchunk, uint64_t *list, uint64_t *best, uint64_t *shared_key, int *count) {
+__device__ void select_top(const RowArgs &a, int64_t base, TopSpace &s) {
     const int k = a.k, tid = threadIdx.x;
     // a lower bound of the k-th best chunk: the k-th of 64 groups' best chunks
-    uint64_t mine = 0;
-    for (int c = tid; c < nchunk; c += NT) mine = max64(mine, key_of(cmax[c], (uint32_t)c));
-    uint64_t grp = mine;
-    grp = max64(grp, shfl_xor64(grp, 1));
-    grp = max64(grp, shfl_xor64(grp, 2));
-    grp = max64(grp, shfl_xor64(grp, 4));
-    if ((tid & 7) == 0) list[tid >> 3] = grp;
-    if (tid == 0) *shared_key = 0, *count = 0;
+    uint64_t grp = 0;
+    for (int c = tid; c < a.chunks; c += NT) grp = max64(grp, key_of(s.cmax[c], (uint32_t)c));
+    grp = max_of_8(grp);
+    if ((tid & 7) == 0) s.list[tid >> 3] = grp;
+    if (tid == 0) s.bound = 0, s.count = 0;
     __syncthreads();
     if (tid < 64) {
-        const uint64_t key = list[tid];
-        int rank = 0;
-        for (int j = 0; j < 64; ++j) rank += list[j] > key;
-        if (rank == k - 1 && key) *shared_key = key;  // keys other than 0 are distinct
+        const uint64_t key = s.list[tid];
+        if (rank_of(s.list, 64, key) == k - 1 && key) s.bound = key;  // keys other than 0 are distinct
     }
     __syncthreads();
-    const uint64_t bound = *shared_key;
-    __syncthreads();
+    const uint64_t bound = s.bound;
     if (grp >= bound && grp)
-        for (int c = tid; c < nchunk; c += NT) {
-            const uint64_t key = key_of(cmax[c], (uint32_t)c);
+        for (int c = tid; c < a.chunks; c += NT) {
+            const uint64_t key = key_of(s.cmax[c], (uint32_t)c);
             if (key >= bound) {
-                const int at = atomicAdd(count, 1);
-                if (at < CAP) list[at] = key;
+                const int at = atomicAdd(&s.count, 1);
+                if (at < CAP) s.list[at] = key;
             }
         }
     __syncthreads();
-    const int n = *count;
+    const int n = s.count;
     if (n <= CAP) {
-        rank_select(list, n, best, k);
+        rank_select(s.list, n, s.best, k);
     } else {
         // far more chunks above the bound than usual: one by one
         uint64_t last = ~0ull;
         for (int i = 0; i < k; ++i) {
             uint64_t top = 0;
-            for (int c = tid; c < nchunk; c += NT) {
-                const uint64_t key = key_of(cmax[c], (uint32_t)c);
+            for (int c = tid; c < a.chunks; c += NT) {
+                const uint64_t key = key_of(s.cmax[c], (uint32_t)c);
                 if (key < last) top = max64(top, key);
             }
-#pragma unroll
-            for (int off = 32; off > 0; off >>= 1) top = max64(top, shfl_xor64(top, off));
-            if ((tid & 63) == 0) list[tid >> 6] = top;
+            top = max_of_8(top);
+            if ((tid & 7) == 0) s.list[tid >> 3] = top;
             __syncthreads();
-            for (int j = 0; j < NT / 64; ++j) top = max64(top, list[j]);
-            if (tid == 0) best[i] = top;
+            for (int j = 0; j < NT / 8; ++j) top = max64(top, s.list[j]);
+            if (tid == 0) s.best[i] = top;
             last = top;
             __syncthreads();
         }
     }
-    // the elements of the k chunks that reach the k-th chunk's maximum
-    const uint64_t floor = best[k - 1] >> 32;
-    if (tid == 0) *count = 0;
+    // of longer chunks, the runs of CE elements that reach the k-th chunk's maximum
+    if (a.runs > 1) {
+        const uint64_t floor = s.best[k - 1] >> 32;
+        if (tid == 0) s.count = 0;
+        __syncthreads();
+        for (int i = tid; i < k * a.runs; i += NT) {  // at most CAP
+            const uint64_t ck = s.best[i / a.runs];
+            const uint32_t r = ~(uint32_t)ck * (uint32_t)a.runs + (uint32_t)(i % a.runs);
+            const int64_t e = (int64_t)r * CE;
+            if (!ck || e >= a.vocab) continue;
+            float top = load1<T>(a.x, base + e);
+            for (int q = 1; q < CE && e + q < a.vocab; ++q) top = fmaxf(top, load1<T>(a.x, base + e + q));
+            const uint64_t key = key_of(top, r);
+            if ((key >> 32) >= floor) s.list[atomicAdd(&s.count, 1)] = key;
+        }
+        __syncthreads();
+        rank_select(s.list, s.count, s.best, k);
+    }
+    // the elements of the k runs that reach the k-th one's maximum
+    const uint64_t floor = s.best[k - 1] >> 32;
+    if (tid == 0) s.count = 0;
     __syncthreads();
-    for (int i = tid; i < k * CE; i += NT) {
-        const uint64_t ck = best[i / CE];
-        const int64_t e = e0 + (int64_t)(uint32_t)~(uint32_t)ck * CE + i % CE;
-        if (ck && e < e1) {
+    for (int i = tid; i < k * CE; i += NT) {  // at most CAP
+        const uint64_t ck = s.best[i / CE];
+        const int64_t e = (int64_t)(uint32_t)~(uint32_t)ck * CE + i % CE;
+        if (ck && e < a.vocab) {
             const uint64_t key = key_of(load1<T>(a.x, base + e), (uint32_t)e);
-            if ((key >> 32) >= floor) list[atomicAdd(count, 1)] = key;  // k CE <= CAP
+            if ((key >> 32) >= floor) s.list[atomicAdd(&s.count, 1)] = key;
         }
     }
     __syncthreads();
-    rank_select(list, *count, best, k);
+    rank_select(s.list, s.count, s.best, k);
 }
 
-// One segment of one row.
+// One row.
 template <int T>
 __global__ __launch_bounds__(NT) void row_kernel(RowArgs a) {
-    __shared__ float cmax[SEG_CHUNKS];
-    __shared__ uint64_t list[CAP], best[KMAX], shared_key;
+    __shared__ TopSpace top;
     __shared__ Stats wave_part[NT / 64];
-    __shared__ int count;
     __shared__ float row_lse;
-    const int tid = threadIdx.x;
-    const int64_t row = blockIdx.x / a.segs, sg = blockIdx.x - row * a.segs;
-    const int64_t e0 = sg * a.seg, e1 = min(a.vocab, e0 + a.seg);
-    const int nchunk = (int)((e1 - e0 + CE - 1) / CE);
-    const int64_t base = row * a.ld;
-    Stats st = {-3.4028235e38f, 0.0f, 0.0f};
-    for (int c = tid; c < nchunk; c += NT) {
-        const int64_t e = e0 + (int64_t)c * CE;
-        float x[CE];
-        if (e + CE <= e1) {
-            load8<T>(a.x, base + e, 8, x);
-            load8<T>(a.x, base + e + 8, 8, x + 8);
-        } else {
-#pragma unroll
-            for (int q = 0; q < CE; ++q) x[q] = e + q < e1 ? load1<T>(a.x, base + e + q) : -INFINITY;
-        }
-        float cm = x[0];
-#pragma unroll
-        for (int q = 1; q < CE; ++q) cm = fmaxf(cm, x[q]);
-        cmax[c] = cm;
-        if (cm > st.m) {
-            const float d = st.m - cm, f = __expf(d);
-            st.t = f * (st.t + st.s * fmaxf(d, -200.0f));
-            st.s *= f;
-            st.m = cm;
-        }
-#pragma unroll
-        for (int q = 0; q < CE; ++q) {
-            const float d = x[q] - st.m;  // NaN stays NaN in the sum s
-            const float e1x = __expf(d);
-            st.s += e1x;
-            st.t += e1x * fmaxf(d, -200.0f);  // 0 where e^d vanishes, for d = -inf too
-        }
-    }
-    st = wave_stats(st);
-    if ((tid & 63) == 0) wave_part[tid >> 6] = st;
-    __syncthreads();
-    if (tid == 0) {
-        st = wave_part[0];
-        for (int i = 1; i < NT / 64; ++i) st = merge(st, wave_part[i]);
-        if (a.segs == 1)
-            row_lse = finish_row<T>(a, row, st);
-        else
-            a.part[blockIdx.x] = st;
-    }
+    const int64_t row = blockIdx.x, base = row * a.ld;
+    Target target = {-1, 0.0f};
+    if (threadIdx.x == 0) target = target_of<T>(a, row);
+    Stats st = take_chunks<T, NT>(a, base, 0, a.chunks, a.k ? top.cmax : nullptr);
+    st = block_stats<NT>(st, wave_part);
+    if (threadIdx.x == 0) row_lse = finish_row(a, row, st, target);
     if (a.k == 0) return;
     __syncthreads();
-    segment_top<T>(a, base, e0, e1, cmax, nchunk, list, best, &shared_key, &count);
-    if (a.segs == 1)
-        write_top(a, row, best, row_lse);
-    else
-        for (int i = tid; i < a.k; i += NT) a.part_top[(int64_t)blockIdx.x * a.k + i] = best[i];
+    select_top<T>(a, base, top);
+    write_top(a, row, top.best, row_lse);
 }
 
-// Joins a row's segments, in their order.
+// One part of a row.
 template <int T>
-__global__ __launch_bounds__(256) void join_kernel(RowArgs a) {
-    __shared__ uint64_t list[CAP], best[KMAX], bound;
-    __shared__ int count;
+__global__ __launch_bounds__(NTS) void part_kernel(RowArgs a) {
+    __shared__ Stats wave_part[NTS / 64];
+    const int64_t row = blockIdx.x / a.segs;
+    const int sg = (int)(blockIdx.x - row * a.segs);
+    const int c0 = sg * a.per_seg, c1 = min(a.chunks, c0 + a.per_seg);
+    Stats st = take_chunks<T, NTS>(a, row * a.ld, c0, c1, a.k ? a.maxima + row * a.chunks : nullptr);
+    st = block_stats<NTS>(st, wave_part);
+    if (threadIdx.x == 0) a.part[blockIdx.x] = st;
+}
+
+// Joins a row's parts: statistics in a fixed order, and the selection.
+template <int T>
+__global__ __launch_bounds__(NT) void join_kernel(RowArgs a) {
+    __shared__ TopSpace top;
     __shared__ float row_lse;
     const int64_t row = blockIdx.x;
-    const int tid = threadIdx.x;
-    if (tid == 0) {
-        Stats st = a.part[row * a.segs];
-        for (int i = 1; i < a.segs; ++i) st = merge(st, a.part[row * a.segs + i]);
-        row_lse = finish_row<T>(a, row, st);
-        count = 0;
-        // the best of the segments' k-th keys is a lower bound of the row's k-th
-        uint64_t b = 0;
-        for (int i = 0; i < a.segs && a.k; ++i)
-            b = max64(b, a.part_top[(row * a.segs + i) * a.k + a.k - 1]);
-        bound = b;
+    Target target = {-1, 0.0f};
+    if (threadIdx.x == 0) target = target_of<T>(a, row);
+    if (a.k)
+#pragma unroll 8
+        for (int c = threadIdx.x; c < a.chunks; c += NT) top.cmax[c] = a.maxima[row * a.chunks + c];
+    if (threadIdx.x < 64) {
+        Stats st = {-3.4028235e38f, 0.0f, 0.0f};
+        for (int i = threadIdx.x; i < a.segs; i += 64) st = merge(st, a.part[row * a.segs + i]);
+        st = wave_stats(st);
+        if (threadIdx.x == 0) row_lse = finish_row(a, row, st, target);
     }
     if (a.k == 0) return;
     __syncthreads();
-    const int total = a.segs * a.k;
-    const uint64_t *top = a.part_top + row * total;
-    // total <= CAP, so the list holds every key
-    for (int i = tid; i < total; i += 256)
-        if (top[i] >= bound && top[i]) list[atomicAdd(&count, 1)] = top[i];
-    __syncthreads();
-    rank_select(list, count, best, a.k);
-    write_top(a, row, best, row_lse);
+    select_top<T>(a, row * a.ld, top);
+    write_top(a, row, top.best, row_lse);
 }
 
 // d logits = -p (g + g_H (log p + H)), and g more at the target.
@@ -336,19 +399,30 @@ __global__ __launch_bounds__(256) void grad_kernel(const char *__restrict__ x, i
     }
 }
 
-// Elements of a segment: a whole row, or less where there are too few rows to
-// give every CU work (512 workgroups), but no less than 8192.
-int64_t segment_of(int64_t rows, int64_t vocab, int32_t k) {
-    const int64_t want = rows >= 512 ? 1 : (512 + rows - 1) / rows;
-    int64_t segs = vocab / 8192 < want ? vocab / 8192 : want;
-    const int64_t most = k > 0 ? CAP / k : 64;  // the join's list
-    if (segs > most) segs = most;
+// How a launch is laid out.  A workgroup to a row where there are rows for every CU,
+// or where a row is short; else parts of no less than 4096 elements, up to about 1024
+// of them (8 rows of 131072 bf16 logits, k = 20: 13 us in 32 parts a row).
+void layout(RowArgs &a) {
+    a.runs = (int)((a.vocab + (int64_t)CHUNKS * CE - 1) / ((int64_t)CHUNKS * CE));
+    a.chunks = (int)((a.vocab + a.runs * CE - 1) / (a.runs * CE));
+    int64_t segs = a.rows >= 512 ? 1 : (1024 + a.rows - 1) / a.rows;
+    if (segs > a.chunks / NTS) segs = a.chunks / NTS;
     if (segs < 1) segs = 1;
-    int64_t seg = round_up((vocab + segs - 1) / segs, CE);
-    return seg < SEG ? seg : SEG;
+    a.per_seg = (int)round_up((a.chunks + segs - 1) / segs, NTS);
+    a.segs = (a.chunks + a.per_seg - 1) / a.per_seg;
 }
 
-constexpr int64_t MAX_VOCAB = SEG * (CAP / KMAX);  // 2^21
+template <int T>
+void launch_rows(const RowArgs &a, hipStream_t s) {
+    if (a.segs == 1) {
+        hipLaunchKernelGGL(row_kernel<T>, dim3((unsigned)a.rows), dim3(NT), 0, s, a);
+        return;
+    }
+    hipLaunchKernelGGL(part_kernel<T>, dim3((unsigned)(a.rows * a.segs)), dim3(NTS), 0, s, a);
+    hipLaunchKernelGGL(join_kernel<T>, dim3((unsigned)a.rows), dim3(NT), 0, s, a);
+}
+
+constexpr int64_t MAX_VOCAB = (int64_t)CHUNKS * CE * (CAP / KMAX);  // 2^21
 constexpr int64_t MAX_ROWS = int64_t(1) << 24;
 
 }  // namespace
@@ -358,9 +432,11 @@ using namespace bakron;
 
 extern "C" size_t bakron_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int32_t k) {
     if (rows < 1 || rows > MAX_ROWS || vocab < 1 || vocab > MAX_VOCAB || k < 0 || k > KMAX || k > vocab) return 0;
-    const int64_t seg = segment_of(rows, vocab, k), segs = (vocab + seg - 1) / seg;
-    if (segs == 1) return 0;
-    return align256(rows * segs * sizeof(Stats)) + align256(rows * segs * k * sizeof(uint64_t));
+    RowArgs a = {};
+    a.rows = rows, a.vocab = vocab;
+    layout(a);
+    if (a.segs == 1) return 0;
+    return align256(rows * a.segs * sizeof(Stats)) + (k ? align256(rows * a.chunks * sizeof(float)) : 0);
 }
 
 extern "C" int32_t bakron_token_logprobs(const void *logits, int32_t type, int64_t rows, int64_t vocab,
@@ -380,8 +456,8 @@ extern "C" int32_t bakron_token_logprobs(const void *logits, int32_t type, int64
     BK_REQUIRE((reinterpret_cast<uintptr_t>(logits) & (elem_size(type) - 1)) == 0,
                "logits are misaligned for their type");
     RowArgs a = {};
-    a.seg = segment_of(rows, vocab, k);
-    a.segs = (int)((vocab + a.seg - 1) / a.seg);
+    a.rows = rows, a.vocab = vocab;
+    layout(a);
     const size_t need = bakron_token_logprobs_workspace_size(rows, vocab, k);
     if (need && (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255))) {
         set_error("workspace must be 256-byte aligned and hold %zu bytes (got %zu)", need, ws_bytes);
@@ -391,32 +467,21 @@ extern "C" int32_t bakron_token_logprobs(const void *logits, int32_t type, int64
     if (st != BAKRON_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream_);
     a.x = static_cast<const char *>(logits);
-    a.rows = rows, a.vocab = vocab, a.ld = ld, a.targets = targets, a.k = k;
+    a.ld = ld, a.targets = targets, a.k = k;
     a.logprob = logprob, a.lse = lse, a.entropy = entropy;
     a.top_logprob = top_logprob, a.top_ids = top_ids, a.dev_status = dev_status;
     if (a.segs > 1) {
         Carver c(ws);
         a.part = c.take<Stats>(rows * a.segs);
-        a.part_top = c.take<uint64_t>(rows * a.segs * k);
+        a.maxima = c.take<float>(k ? rows * a.chunks : 0);
     }
-    const dim3 grid((unsigned)(rows * a.segs));
     if (type == BAKRON_T_F32)
-        hipLaunchKernelGGL(row_kernel<BAKRON_T_F32>, grid, dim3(NT), 0, s, a);
+        launch_rows<BAKRON_T_F32>(a, s);
     else if (type == BAKRON_T_BF16)
-        hipLaunchKernelGGL(row_kernel<BAKRON_T_BF16>, grid, dim3(NT), 0, s, a);
+        launch_rows<BAKRON_T_BF16>(a, s);
     else
-        hipLaunchKernelGGL(row_kernel<BAKRON_T_F16>, grid, dim3(NT), 0, s, a);
-    BK_LAUNCH_CHECK("row_kernel");
-    if (a.segs > 1) {
-        const dim3 jg((unsigned)rows);
-        if (type == BAKRON_T_F32)
-            hipLaunchKernelGGL(join_kernel<BAKRON_T_F32>, jg, dim3(256), 0, s, a);
-        else if (type == BAKRON_T_BF16)
-            hipLaunchKernelGGL(join_kernel<BAKRON_T_BF16>, jg, dim3(256), 0, s, a);
-        else
-            hipLaunchKernelGGL(join_kernel<BAKRON_T_F16>, jg, dim3(256), 0, s, a);
-        BK_LAUNCH_CHECK("join_kernel");
-    }
+        launch_rows<BAKRON_T_F16>(a, s);
+    BK_LAUNCH_CHECK("token log probabilities");
     return BAKRON_OK;
 }
 

@@ -9,6 +9,7 @@
 // fp8 operands carry a scale for each 128 of r, so their products of one K step
 // are summed by themselves and then added with the scale, in fp32.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.hpp"
 #include "elem.hpp"
@@ -172,9 +173,11 @@ __device__ __forceinline__ bool find_work(const ProductArgs &p, Work &t) {
     int64_t w;
     if constexpr (MODE == GRAD_W) {
         const int64_t tiles = (int64_t)p.tiles_i * p.tiles_j;
-        w = xcd_order(b, tiles * p.groups);
-        t.g = (int)(w / tiles);
-        const int n = (int)(w - t.g * tiles);
+        // every XCD gets a part of each group's tiles: groups differ in length (8192 rows
+        // in 16 uneven groups, both gradients: 0.41 against 0.45 ms)
+        t.g = (int)(b / tiles);
+        const int n = (int)xcd_order(b - t.g * tiles, tiles);
+        w = t.g * tiles + n;
         t.tj = n / p.tiles_i;
         t.i0 = (int64_t)(n % p.tiles_i) * BI;
         t.i1 = min<int64_t>(p.I, t.i0 + BI);
@@ -315,68 +318,95 @@ __device__ __forceinline__ floatx4 mfma_f8(intx4 a0, intx4 a1, intx4 b0, intx4 b
 
 // A wave's part of a tile, NI x NJ accumulators: rows from i0 on (below i1), columns
 // from j0 on.  An accumulator's lane holds 4 columns of one row, so stores from there
-// would touch a quarter of a line each; 16 rows at a time go through LDS (`scratch`,
-// 16 * 32 NJ bytes of this wave's own, 64 NJ for fp32) and leave as whole rows, 16
-// bytes a lane.  The 16-byte chunk c of row i lies at place c ^ i.
+// would touch a quarter of a line each; the part goes through LDS (`scratch`, 512 NI NJ
+// bytes of this wave's own; fp32 results in two turns, half of the columns each) and
+// leaves as whole rows, 16 bytes a lane.  The 16-byte chunk c of row r lies at place
+// c ^ r.  One wait between the writes and the reads of a turn: with 4 waves a CU there
+// is little else to run meanwhile (16 rows at a time took twice as long).
 template <int SCALE, int NI, int NJ>
 __device__ __forceinline__ void store_tile(const ProductArgs &p, floatx4 (&acc)[NI][NJ], int g, int64_t yoff,
                                            int64_t i0, int64_t i1, int64_t j0, int lane, char *scratch) {
-    static_assert(NJ % 4 == 0, "a power of two chunks a row");
+    constexpr int CH = 2 * NJ, ROWS = 64 / CH;  // chunks of a row, rows a wave stores at once
+    static_assert((NJ & (NJ - 1)) == 0 && NJ >= 2 && NJ <= 16, "a power of two chunks a row");
     const int l = lane & 15, q = lane >> 4;
     const bool f32 = p.ytype == BAKRON_T_F32;
-    floatx4 w[SCALE == BAKRON_SCALE_ROW ? NJ : 1];
-    if constexpr (SCALE == BAKRON_SCALE_ROW) {
+    const int es = f32 ? 4 : 2, per = 16 / es;
+    // the scales of the wave's columns, one a lane and 64 columns
+    float w[(NJ + 3) / 4];
+    if constexpr (SCALE == BAKRON_SCALE_ROW)
 #pragma unroll
-        for (int b = 0; b < NJ; ++b)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int64_t j = j0 + b * 16 + 4 * q + v;
-                w[b][v] = g < p.groups && j < p.J ? p.sq[g * p.J + j] : 0.0f;
-            }
-    }
-#pragma unroll
-    for (int a = 0; a < NI; ++a) {
-        if (i0 + a * 16 >= i1) break;
+        for (int k = 0; k < (NJ + 3) / 4; ++k) {
+            const int64_t j = j0 + 64 * k + lane;
+            w[k] = g < p.groups && j < p.J ? p.sq[g * p.J + j] : 0.0f;
+        }
+    auto write = [&](auto type, int b0, int b1) __attribute__((always_inline)) {
+        constexpr int T = decltype(type)::value;
 #pragma unroll
         for (int b = 0; b < NJ; ++b) {
-            floatx4 t = acc[a][b];
+            if (b < b0 || b >= b1) continue;
+            float ws[4];
             if constexpr (SCALE == BAKRON_SCALE_ROW)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) t[v] *= w[b][v];
-            if (f32) {
-                *reinterpret_cast<floatx4 *>(scratch + l * 64 * NJ + (((4 * b + q) ^ l) & (4 * NJ - 1)) * 16) = t;
-            } else {
-                uint2 u;
-                if (p.ytype == BAKRON_T_BF16)
-                    u = make_uint2(pack2<BAKRON_T_BF16>(t[0], t[1]), pack2<BAKRON_T_BF16>(t[2], t[3]));
+                for (int v = 0; v < 4; ++v) ws[v] = __shfl(w[b / 4], (b % 4) * 16 + 4 * q + v);
+            const int k = T == BAKRON_T_F32 ? 4 * (b - b0) + q : 2 * b + (q >> 1);
+            char *to = scratch + l * CH * 16 + ((k ^ l) & (CH - 1)) * 16 + (T == BAKRON_T_F32 ? 0 : (q & 1) * 8);
+#pragma unroll
+            for (int a = 0; a < NI; ++a) {
+                floatx4 t = acc[a][b];
+                if constexpr (SCALE == BAKRON_SCALE_ROW)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) t[v] *= ws[v];
+                if constexpr (T == BAKRON_T_F32)
+                    *reinterpret_cast<floatx4 *>(to + a * 16 * CH * 16) = t;
                 else
-                    u = make_uint2(pack2<BAKRON_T_F16>(t[0], t[1]), pack2<BAKRON_T_F16>(t[2], t[3]));
-                const int c = (2 * b + (q >> 1)) ^ l;
-                *reinterpret_cast<uint2 *>(scratch + l * 32 * NJ + (c & (2 * NJ - 1)) * 16 + (q & 1) * 8) = u;
+                    *reinterpret_cast<uint2 *>(to + a * 16 * CH * 16) = make_uint2(pack2<T>(t[0], t[1]), pack2<T>(t[2], t[3]));
             }
         }
+    };
+    const int c = lane % CH, r0 = lane / CH;
+    const bool full = p.vec && i0 + 16 * NI <= i1 && j0 + 16 * NJ <= p.J;
+    const int64_t down = (int64_t)ROWS * p.ldy * es;
+    auto leave = [&](int turn) __attribute__((always_inline)) {
         // the wave's own writes, then reads: in order, no other wave takes part
         __builtin_amdgcn_wave_barrier();
-        const int chunks = f32 ? 4 * NJ : 2 * NJ, per = f32 ? 4 : 8;  // chunks of a row, elements of a chunk
-        for (int k = lane; k < 16 * chunks; k += 64) {
-            const int r = k / chunks, c = k % chunks;
-            const intx4 v = *reinterpret_cast<const intx4 *>(scratch + r * chunks * 16 + ((c ^ r) & (chunks - 1)) * 16);
-            const int64_t i = i0 + a * 16 + r, j = j0 + c * per, left = p.J - j;
-            if (i >= i1 || left <= 0) continue;
-            char *y = p.Y + (yoff + i * p.ldy + j) * (f32 ? 4 : 2);
-            if (left >= per && p.vec) {
-                *reinterpret_cast<intx4 *>(y) = v;
-            } else if (f32) {
+        const int64_t jc = j0 + turn * NJ * 8 + c * per;
+        char *y = p.Y + (yoff + (i0 + r0) * p.ldy + jc) * es;
+        const char *from = scratch + r0 * CH * 16;
+        if (full) {
+#pragma unroll 4
+            for (int r = r0; r < 16 * NI; r += ROWS, from += ROWS * CH * 16, y += down)
+                *reinterpret_cast<intx4 *>(y) = *reinterpret_cast<const intx4 *>(from + ((c ^ r) & (CH - 1)) * 16);
+        } else {
+            const int left = (int)min<int64_t>(per, p.J - jc), rows = (int)min<int64_t>(16 * NI, i1 - i0);
+#pragma unroll 1
+            for (int r = r0; r < rows; r += ROWS, from += ROWS * CH * 16, y += down) {
+                const intx4 v = *reinterpret_cast<const intx4 *>(from + ((c ^ r) & (CH - 1)) * 16);
+                if (left == per && p.vec) {
+                    *reinterpret_cast<intx4 *>(y) = v;
+                } else if (f32) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (e < left) reinterpret_cast<int *>(y)[e] = v[e];
-            } else {
+                    for (int e = 0; e < 4; ++e)
+                        if (e < left) reinterpret_cast<int *>(y)[e] = v[e];
+                } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e < left) reinterpret_cast<uint16_t *>(y)[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+                    for (int e = 0; e < 8; ++e)
+                        if (e < left) reinterpret_cast<uint16_t *>(y)[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+                }
             }
         }
         __builtin_amdgcn_wave_barrier();
+    };
+    if (f32) {
+        write(std::integral_constant<int, BAKRON_T_F32>(), 0, NJ / 2);
+        leave(0);
+        write(std::integral_constant<int, BAKRON_T_F32>(), NJ / 2, NJ);
+        leave(1);
+    } else {
+        if (p.ytype == BAKRON_T_BF16)
+            write(std::integral_constant<int, BAKRON_T_BF16>(), 0, NJ);
+        else
+            write(std::integral_constant<int, BAKRON_T_F16>(), 0, NJ);
+        leave(0);
     }
 }
 
@@ -397,7 +427,7 @@ constexpr int PIECES = 16;
 template <int MODE, int SCALE, int KR>
 __global__ __launch_bounds__(64) void product_join_kernel(ProductArgs p, int parts) {
     constexpr int BI = 128, BJ = 128, NI = 4, NJ = 4;
-    __shared__ __align__(16) char lds[64 * 16 * NJ];
+    __shared__ __align__(16) char lds[512 * NJ];
     const int lane = threadIdx.x;
     Work t;
     p.splits = PIECES;
@@ -532,10 +562,10 @@ __global__ __launch_bounds__(64 * WI * WJ) void product_kernel(ProductArgs p) {
         return;
     }
     // every wave is done with the operands' buffers, which now carry the results
-    static_assert(64 * 16 * NJ * WI * WJ <= (int)sizeof(lds), "the results' 16 rows of each wave");
+    static_assert(512 * NI * NJ * WI * WJ <= (int)sizeof(lds), "the results of each wave");
     __syncthreads();
     store_tile<SCALE, NI, NJ>(p, acc, g, yoff, i0 + wi * (BI / WI), i1, j0 + wj * (BJ / WJ), lane,
-                              lds + wave * 64 * 16 * NJ);
+                              lds + wave * 512 * NI * NJ);
 }
 
 // 16 zero bytes: what a lane loads in the place of r beyond the end.
@@ -804,10 +834,10 @@ __global__ __launch_bounds__(64 * WI * WJ) void product_direct_kernel(ProductArg
         return;
     }
     // every wave is done with the operands' buffers, which now carry the results
-    static_assert(64 * 16 * NJ * WI * WJ <= (int)sizeof(lds), "the results' 16 rows of each wave");
+    static_assert(512 * NI * NJ * WI * WJ <= (int)sizeof(lds), "the results of each wave");
     __syncthreads();
     store_tile<SCALE, NI, NJ>(p, acc, g, yoff, i0 + wi * (BI / WI), i1, j0 + wj * (BJ / WJ), lane,
-                              lds + wave * 64 * 16 * NJ);
+                              lds + wave * 512 * NI * NJ);
 }
 
 // Few rows a group (decoding): the weights stream past once and bound the time, so
