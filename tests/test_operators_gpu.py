@@ -537,3 +537,30 @@ def test_other_stream_and_graph(bk):
         torch.cuda.synchronize()
         assert all(same(a, b) for a, b in zip(want, kept))
         assert all(same(a, b) for a, b in zip(want, all_of()))
+
+
+# ---------------------------------------------------------------- together
+
+@pytest.mark.parametrize("kind,bits", [(0, 4), (1, 3)])
+def test_rounded_experts(bk, kind, bits):
+    """The example: experts rounded, multiplied in fp8 and scored.  The fp8 weights are
+    the solve's V exactly, the product is theirs with the activations as quantised,
+    and the scores are those of the logits."""
+    from two_sided_gptq_amd import experts
+    X, W, head, offsets, targets = experts.example(experts=4, tokens=500, width=192, vocab=1000)
+    r = experts.round_experts(X, W, head, offsets, targets, kind=kind, bits=bits)
+    assert int(r["status"]) == 0
+    at = offsets.tolist()
+    assert at[-1] == 500 and at[-2] == 500  # the last expert has no tokens
+    Vd = r["W8"].double() * r["scales"].double()[:, :, None]
+    err = (Vd - r["V"].double()).abs()
+    assert bool((err <= 2.0 ** -23 * Vd.abs()).all())
+    col = torch.arange(192, device="cuda") // 128
+    Xd = r["X8"].double() * r["sx"].double()[col].t()
+    for e in range(4):
+        a, b = at[e], at[e + 1]
+        want, mass = Xd[a:b] @ Vd[e].t(), Xd[a:b].abs() @ Vd[e].abs().t()
+        assert bool(((r["Y8"][a:b].double() - want).abs() <= U["bf16"] * want.abs() + 2.0 ** -12 * mass).all())
+    # rounding to 4 bits costs little of the scores, to 3 more, and both change them
+    loss = float((r["before"]["logprob"] - r["after"]["logprob"]).mean())
+    assert loss != 0.0 and abs(loss) < (0.5 if bits == 4 else 2.0), loss
