@@ -337,11 +337,12 @@ def _vector(t, name, dtype, shape):
 
 
 def _out(out, shape, dtype, device, name):
+    """(the output, the element distance between its rows): `out` after checks, or new."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device), shape[-1]
     if out.shape != shape or out.dtype != dtype:
         raise BakronError(f"{name} must be {dtype} of shape {tuple(shape)}")
-    return out
+    return out, _rows_of(out, name, (dtype,), len(shape))
 
 
 def _where(stream, *tensors):
@@ -369,10 +370,10 @@ def fp8_quantize(X, block_rows=1, out=None, scales=None, dev_status=None, stream
     rows, cols = X.shape
     if block_rows not in (1, 128):
         raise BakronError(f"block_rows must be 1 or 128, not {block_rows}")
-    Q = _out(out, (rows, cols), _FP8, X.device, "out")
-    ldq = _rows_of(Q, "out", (_FP8,))
-    S = _out(scales, (-(-cols // 128), -(-rows // block_rows)), torch.float32, X.device, "scales")
-    sp = _vector(S, "scales", torch.float32, S.shape)
+    Q, ldq = _out(out, (rows, cols), _FP8, X.device, "out")
+    of = (-(-cols // 128), -(-rows // block_rows))
+    S = torch.empty(of, dtype=torch.float32, device=X.device) if scales is None else scales
+    sp = S.data_ptr() if scales is None else _vector(S, "scales", torch.float32, of)
     _check(lib.bakron_fp8_quantize(X.data_ptr(), _TYPES[X.dtype], rows, cols, ldx, block_rows, Q.data_ptr(),
                                    ldq, sp, _status(dev_status), _where(stream, Q, S)), "bakron_fp8_quantize")
     return Q, S
@@ -386,8 +387,7 @@ def fp8_from_codes(codes, zeros=None, kind=Q_SYM, bits=4, out=None, stream=None)
     m, n = codes.shape
     cp = _vector(codes, "codes", torch.int8, (m, n))
     zp = None if zeros is None else _vector(zeros, "zeros", torch.float32, (m,))
-    Q = _out(out, (m, n), _FP8, codes.device, "out")
-    ldq = _rows_of(Q, "out", (_FP8,))
+    Q, ldq = _out(out, (m, n), _FP8, codes.device, "out")
     _check(lib.bakron_fp8_from_codes(cp, zp, m, n, kind, bits, Q.data_ptr(), ldq, _where(stream, Q)),
            "bakron_fp8_from_codes")
     return Q
@@ -430,8 +430,7 @@ def fp8_matmul(X, sx, W, sw, offsets=None, out_dtype=torch.bfloat16, out=None, d
         wscale, swp = SCALE_ROW, _vector(sw, "sw", torch.float32, (*lead, N))
     if out_dtype not in (torch.bfloat16, torch.float16):
         raise BakronError(f"out_dtype must be bfloat16 or float16, not {out_dtype}")
-    Y = _out(out, (rows, N), out_dtype, X.device, "out")
-    ldy = _rows_of(Y, "out", _TYPES)
+    Y, ldy = _out(out, (rows, N), out_dtype, X.device, "out")
     ws = _space(lib.bakron_fp8_matmul_workspace_size(rows, N, K, groups), X.device)
     _check(lib.bakron_fp8_matmul(X.data_ptr(), ldx, sxp, W.data_ptr(), ldw, swp, wscale, rows, N, K, groups,
                                  op, Y.data_ptr(), _TYPES[out_dtype], ldy, _status(dev_status),
@@ -447,8 +446,7 @@ def _grouped(fn, what, A, B, rows, N, K, groups, op, shape, out_dtype, out, dev_
     dtype = A.dtype if out_dtype is None else out_dtype
     if dtype not in (A.dtype, torch.float32):
         raise BakronError(f"the output's dtype must be {A.dtype} or float32, not {dtype}")
-    Y = _out(out, shape, dtype, A.device, "out")
-    ldy = _rows_of(Y, "out", (dtype,), len(shape))
+    Y, ldy = _out(out, shape, dtype, A.device, "out")
     ws = _space(lib.bakron_grouped_matmul_workspace_size(rows, N, K, groups), A.device)
     _check(fn(A.data_ptr(), _TYPES[A.dtype], lda, B.data_ptr(), ldb, rows, N, K, groups, op, Y.data_ptr(),
               _TYPES[dtype], ldy, _status(dev_status), None if ws is None else ws.data_ptr(),
@@ -520,8 +518,7 @@ def token_logprobs_grad(logits, targets, lse, entropy, g_logprob, g_entropy=None
     ld = _rows_of(logits, "logits", _TYPES)
     rows, vocab = logits.shape
     f32 = torch.float32
-    D = _out(out, (rows, vocab), logits.dtype, logits.device, "out")
-    ldd = _rows_of(D, "out", (logits.dtype,))
+    D, ldd = _out(out, (rows, vocab), logits.dtype, logits.device, "out")
     if g_entropy is not None and entropy is None:
         raise BakronError("g_entropy needs the forward call's entropy")
     _check(lib.bakron_token_logprobs_grad(

@@ -1039,12 +1039,10 @@ void launch(ProductArgs &p, hipStream_t s) {
         splits = choose_splits(MODE, p.rows, p.I, p.J, steps_of(MODE, ES, p.rows, p.R, p.groups), p.groups, p.offsets != nullptr);
     }
     if (direct && large_tiles(MODE, p.rows, p.I, p.J, p.groups, p.offsets != nullptr)) {
-        // Forward, 4 waves hold 128 x 128 accumulators each (bf16 8192 x 8192 x 8192 0.754
-        // against 0.797 ms with 8 waves of 64 x 128).  The gradients' reductions are
-        // shorter and start more often, which 8 waves do faster (16 groups of 8192 rows,
-        // 4096 x 2048: 0.438 against 0.486 ms).  fp8 sums are added by vector
-        // instructions, which cannot use the registers that 4 waves need.
-        constexpr int WI = MODE == FWD && ET != F8 ? 2 : 4;
+        // 4 waves hold 128 x 128 accumulators each: a third less of LDS reads than 8 waves
+        // of 64 x 128 (bf16 8192 x 8192 x 8192 0.754 against 0.797 ms).  fp8 sums are added
+        // by vector instructions, which cannot use the registers that 4 waves need.
+        constexpr int WI = ET == F8 ? 4 : 2;
         const unsigned grid = grid_of<MODE, 256, 256>(p);
         hipLaunchKernelGGL((product_direct_kernel<ET, MODE, SCALE, 256, 256, WI, 2>), dim3(grid),
                            dim3(128 * WI), 0, s, p);
