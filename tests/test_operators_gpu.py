@@ -160,6 +160,8 @@ FP8_CASES = [
     (64, 130, 77, 5, "block", "bf16", 3), (2500, 300, 256, 3, "row", "bf16", 0), (4200, 1100, 640, 2, "block", "bf16", 0),
     # enough tiles for the large ones
     (4100, 2120, 656, 3, "row", "bf16", 0), (4100, 2120, 912, 1, "block", "f16", 16), (4100, 2125, 144, 1, "block", "bf16", 0),
+    # a little over one round of large tiles: the rest in small ones
+    (4100, 4216, 272, 1, "block", "bf16", 0), (4100, 4200, 400, 3, "row", "f16", 8),
     # few rows: the form for single tokens, its widths and ends
     (1, 4096, 1040, 1, "block", "bf16", 0), (2, 40, 2500, 1, "row", "f16", 1), (20, 1000, 384, 1, "block", "bf16", 0),
     (50, 333, 640, 1, "row", "bf16", 0), (64, 512, 129, 1, "block", "f16", 0), (30, 272, 400, 16, "row", "bf16", 0),
@@ -222,6 +224,9 @@ GROUPED_CASES = [
     # enough tiles for the large ones: forward, gradient of X, gradient of W
     (4100, 2120, 328, 3, "bf16", None, 0, 0), (4100, 328, 2120, 2, "f16", "f32", 8, 8), (700, 2056, 1416, 3, "bf16", None, 0, 0),
     (4100, 2128, 264, 1, "f16", "f32", 0, 0),
+    # a little over one round of large tiles, the rest in small ones: forward, gradient of X, gradient of W
+    (4100, 4216, 200, 3, "bf16", None, 0, 0), (4100, 200, 4216, 1, "f16", None, 0, 0), (4100, 136, 4300, 2, "bf16", "f32", 0, 0),
+    (400, 2616, 2632, 3, "bf16", None, 0, 0),
     # few rows
     (1, 300, 1000, 1, "bf16", None, 0, 0), (2, 33, 2050, 1, "f16", "f32", 1, 1), (60, 1000, 200, 1, "bf16", None, 0, 0),
     (90, 130, 520, 7, "bf16", "f32", 0, 0), (33, 272, 264, 40, "f16", None, 0, 0),

@@ -47,6 +47,7 @@ struct ProductArgs {
     int vec;                 // 1: rows of C start on 16 bytes
     int splits;              // parts of the reduction, each a workgroup of its own
     float *part;             // with splits > 1: the parts' sums, as the accumulators hold them
+    int tail;                // 1: large tiles but for the tail; 2: the tail, in small tiles
 };
 
 // A value that is the same in every lane, in a scalar register.
@@ -94,6 +95,14 @@ __device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t total) {
     return x * q + min(x, r) + (b >> 3);
 }
 
+// How many of `total` large tiles a launch of them takes.  A last round that would use
+// half of the 256 CUs or less is left to a second launch, whose small tiles, four to a
+// large one, take two thirds of a round's time or less.
+__host__ __device__ __forceinline__ int64_t without_tail(int64_t total) {
+    const int64_t rem = total & 255;
+    return total > 256 && rem <= 128 ? total - rem : total;
+}
+
 // Finds the workgroup's rows: tiles of BI rows are counted group by group, then
 // walked in bands of 8 row tiles.  All 64 lanes of a wave take part; the results are
 // wave uniform.  False: no work for this workgroup.
@@ -119,9 +128,14 @@ __device__ __forceinline__ bool find_rows(const ProductArgs &p, int64_t b, int &
         for (int base = 64; base <= p.groups; base += 64)
             slots += __builtin_amdgcn_readlane(wave_scan(tiles_of(base + lane)), 63);
     }
-    const int64_t total = (int64_t)slots * p.tiles_j;
-    if (b >= total) return false;
-    w = xcd_order(b, total);
+    const int64_t total = (int64_t)slots * p.tiles_j, most = p.tail ? without_tail(total) : total;
+    if (p.tail == 2) {
+        w = most + b;
+        if (w >= total) return false;
+    } else {
+        if (b >= most) return false;
+        w = xcd_order(b, most);
+    }
     const int64_t per_band = 8 * (int64_t)p.tiles_j;
     const int64_t band = w / per_band, in = w - band * per_band;
     const int width = (int)min<int64_t>(8, slots - band * 8);
@@ -167,20 +181,26 @@ struct Work {
 template <int MODE, int BI, int KR>
 __device__ __forceinline__ bool find_work(const ProductArgs &p, Work &t) {
     report_offsets(p);
-    const int64_t b = blockIdx.x / p.splits;
-    const int part = blockIdx.x % p.splits;
+    // in the tail, four workgroups share a large tile
+    constexpr int LARGE = 256;
+    const bool tail = BI < LARGE && p.tail == 2;
+    const int64_t b = tail ? blockIdx.x >> 2 : blockIdx.x / p.splits;
+    const int part = tail ? 0 : blockIdx.x % p.splits, quarter = tail ? blockIdx.x & 3 : 0;
+    const int size = tail ? LARGE : BI;
     t.P = p.P, t.Q = p.Q, t.R = p.R, t.yoff = 0;
     int64_t w;
     if constexpr (MODE == GRAD_W) {
-        const int64_t tiles = (int64_t)p.tiles_i * p.tiles_j;
+        const int64_t tiles = (int64_t)p.tiles_i * p.tiles_j, total = tiles * p.groups;
+        const int64_t most = p.tail ? without_tail(total) : total, at = p.tail == 2 ? most + b : b;
+        if (at >= (p.tail == 2 ? total : most)) return false;
         // every XCD gets a part of each group's tiles: groups differ in length (8192 rows
         // in 16 uneven groups, both gradients: 0.41 against 0.45 ms)
-        t.g = (int)(b / tiles);
-        const int n = (int)xcd_order(b - t.g * tiles, tiles);
+        t.g = (int)(at / tiles);
+        const int n = (int)xcd_order(at - t.g * tiles, tiles);
         w = t.g * tiles + n;
         t.tj = n / p.tiles_i;
-        t.i0 = (int64_t)(n % p.tiles_i) * BI;
-        t.i1 = min<int64_t>(p.I, t.i0 + BI);
+        t.i0 = (int64_t)(n % p.tiles_i) * size;
+        t.i1 = min<int64_t>(p.I, t.i0 + size);
         int64_t a, z;
         group_range(p, t.g, a, z);
         a = uniform(a);
@@ -189,13 +209,20 @@ __device__ __forceinline__ bool find_work(const ProductArgs &p, Work &t) {
         t.Q += a * p.ldq;
         t.yoff = t.g * p.group_y;
     } else {
-        if (!find_rows<BI>(p, b, t.g, t.i0, t.i1, t.tj, w)) return false;
+        if (tail ? !find_rows<LARGE>(p, b, t.g, t.i0, t.i1, t.tj, w) : !find_rows<BI>(p, b, t.g, t.i0, t.i1, t.tj, w))
+            return false;
         t.g = (int)uniform(t.g), t.tj = (int)uniform(t.tj);
         t.i0 = uniform(t.i0), t.i1 = uniform(t.i1);
         if (t.g == p.groups)
             t.R = 0;  // rows of no group
         else
             t.Q += t.g * p.group_q;
+    }
+    if (tail) {
+        t.i0 += quarter % 2 * BI;
+        t.i1 = min<int64_t>(t.i1, t.i0 + BI);
+        t.tj = t.tj * (LARGE / BI) + quarter / 2;
+        if (t.i0 >= t.i1 || (int64_t)t.tj * BI >= p.J) return false;
     }
     t.nth = uniform(w) * p.splits + part;
     t.s0 = 0;
@@ -958,11 +985,13 @@ int64_t count_tiles(int mode, int64_t b, int64_t rows, int64_t I, int64_t J, int
 // chip (bf16 8192 x 8192 x 8192: 0.75 against 0.94 ms).  A launch of few tiles leaves
 // CUs idle (fp8 2048 x 4096 x 4096: 51 against 41 us), and every group ends in a
 // partial tile.  So: the rounds that each takes on 256 CUs (two small tiles fit on a
-// CU), a round of large ones taking 1.5 times as long as one of small ones.
+// CU), a round of large ones taking 1.5 times as long as one of small ones, or of a
+// tail in small ones.
 bool large_tiles(int mode, int64_t rows, int64_t I, int64_t J, int groups, bool grouped) {
     const int64_t big = count_tiles(mode, 256, rows, I, J, groups, grouped);
     const int64_t small = count_tiles(mode, 128, rows, I, J, groups, grouped);
-    return (big + 255) / 256 * 3 <= (small + 511) / 512 * 2;
+    const int64_t whole = without_tail(big);
+    return (whole + 255) / 256 * 3 + (whole < big ? 2 : 0) <= (small + 511) / 512 * 2;
 }
 
 // Into how many parts the reduction is split where small tiles are few: a step of a
@@ -1044,8 +1073,14 @@ void launch(ProductArgs &p, hipStream_t s) {
         // by vector instructions, which cannot use the registers that 4 waves need.
         constexpr int WI = ET == F8 ? 4 : 2;
         const unsigned grid = grid_of<MODE, 256, 256>(p);
+        // with groups of rows only the device knows how many tiles there are
+        p.tail = MODE != GRAD_W && p.offsets ? grid > 256 : without_tail(grid) < grid;
         hipLaunchKernelGGL((product_direct_kernel<ET, MODE, SCALE, 256, 256, WI, 2>), dim3(grid),
                            dim3(128 * WI), 0, s, p);
+        if (p.tail) {
+            p.tail = 2;
+            hipLaunchKernelGGL((product_direct_kernel<ET, MODE, SCALE, 128, 128, 2, 2>), dim3(4 * 128), dim3(256), 0, s, p);
+        }
         return;
     }
     const unsigned grid = grid_of<MODE, 128, 128>(p);
