@@ -401,7 +401,7 @@ __global__ __launch_bounds__(256) void grad_kernel(const char *__restrict__ x, i
 
 // How a launch is laid out.  A workgroup to a row where there are rows for every CU,
 // or where a row is short; else parts of no less than 4096 elements, up to about 1024
-// of them (8 rows of 131072 bf16 logits, k = 20: 13 us in 32 parts a row).
+// of them (8 rows of 131072 bf16 logits, k = 20: 14 us in 32 parts a row).
 void layout(RowArgs &a) {
     a.runs = (int)((a.vocab + (int64_t)CHUNKS * CE - 1) / ((int64_t)CHUNKS * CE));
     a.chunks = (int)((a.vocab + a.runs * CE - 1) / (a.runs * CE));

@@ -97,7 +97,8 @@ __device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t total) {
 
 // How many of `total` large tiles a launch of them takes.  A last round that would use
 // half of the 256 CUs or less is left to a second launch, whose small tiles, four to a
-// large one, take two thirds of a round's time or less.
+// large one, take two thirds of a round's time or less (bf16, 16384 rows by 8 groups of
+// 11008 x 4096: 1.19 against 1.26 ms; 8192 x 4352 x 1024: 80 against 87 us).
 __host__ __device__ __forceinline__ int64_t without_tail(int64_t total) {
     const int64_t rem = total & 255;
     return total > 256 && rem <= 128 ? total - rem : total;
