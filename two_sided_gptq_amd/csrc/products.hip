@@ -182,11 +182,11 @@ struct Work {
 template <int MODE, int BI, int KR>
 __device__ __forceinline__ bool find_work(const ProductArgs &p, Work &t) {
     report_offsets(p);
-    // in the tail, four workgroups share a large tile
+    // in the tail, four workgroups of one XCD share a large tile
     constexpr int LARGE = 256;
     const bool tail = BI < LARGE && p.tail == 2;
-    const int64_t b = tail ? blockIdx.x >> 2 : blockIdx.x / p.splits;
-    const int part = tail ? 0 : blockIdx.x % p.splits, quarter = tail ? blockIdx.x & 3 : 0;
+    const int64_t b = tail ? (blockIdx.x >> 5 << 3) + (blockIdx.x & 7) : blockIdx.x / p.splits;
+    const int part = tail ? 0 : blockIdx.x % p.splits, quarter = tail ? blockIdx.x >> 3 & 3 : 0;
     const int size = tail ? LARGE : BI;
     t.P = p.P, t.Q = p.Q, t.R = p.R, t.yoff = 0;
     int64_t w;
@@ -199,8 +199,12 @@ __device__ __forceinline__ bool find_work(const ProductArgs &p, Work &t) {
         t.g = (int)(at / tiles);
         const int n = (int)xcd_order(at - t.g * tiles, tiles);
         w = t.g * tiles + n;
-        t.tj = n / p.tiles_i;
-        t.i0 = (int64_t)(n % p.tiles_i) * size;
+        // in bands of 4 rows of tiles: an XCD's part is about square, so its L2 fetches
+        // less (135 against 280 MB there, 0.38 against 0.39 ms)
+        const int band = n / (4 * p.tiles_j), left = n - band * 4 * p.tiles_j;
+        const int high = min(4, p.tiles_i - band * 4);
+        t.tj = left / high;
+        t.i0 = (int64_t)(band * 4 + left % high) * size;
         t.i1 = min<int64_t>(p.I, t.i0 + size);
         int64_t a, z;
         group_range(p, t.g, a, z);
@@ -350,8 +354,11 @@ __device__ __forceinline__ floatx4 mfma_f8(intx4 a0, intx4 a1, intx4 b0, intx4 b
 // bytes of this wave's own; fp32 results in two turns, half of the columns each) and
 // leaves as whole rows, 16 bytes a lane.  The 16-byte chunk c of row r lies at place
 // c ^ r.  One wait between the writes and the reads of a turn: with 4 waves a CU there
-// is little else to run meanwhile (16 rows at a time took twice as long).
-template <int SCALE, int NI, int NJ>
+// is little else to run meanwhile (16 rows at a time took twice as long).  PAST: large
+// tiles' results go past the caches, which keep the operands (gradients of 8192 rows by
+// 16 groups of 4096 x 2048: 0.36 against 0.38 ms; 27 MB of results from small tiles are
+// slower that way, 34.6 against 33.4 us).
+template <int SCALE, int NI, int NJ, bool PAST>
 __device__ __forceinline__ void store_tile(const ProductArgs &p, floatx4 (&acc)[NI][NJ], int g, int64_t yoff,
                                            int64_t i0, int64_t i1, int64_t j0, int lane, char *scratch) {
     constexpr int CH = 2 * NJ, ROWS = 64 / CH;  // chunks of a row, rows a wave stores at once
@@ -402,8 +409,13 @@ __device__ __forceinline__ void store_tile(const ProductArgs &p, floatx4 (&acc)[
         const char *from = scratch + r0 * CH * 16;
         if (full) {
 #pragma unroll 4
-            for (int r = r0; r < 16 * NI; r += ROWS, from += ROWS * CH * 16, y += down)
-                *reinterpret_cast<intx4 *>(y) = *reinterpret_cast<const intx4 *>(from + ((c ^ r) & (CH - 1)) * 16);
+            for (int r = r0; r < 16 * NI; r += ROWS, from += ROWS * CH * 16, y += down) {
+                const intx4 v = *reinterpret_cast<const intx4 *>(from + ((c ^ r) & (CH - 1)) * 16);
+                if constexpr (PAST)
+                    __builtin_nontemporal_store(v, reinterpret_cast<intx4 *>(y));
+                else
+                    *reinterpret_cast<intx4 *>(y) = v;
+            }
         } else {
             const int left = (int)min<int64_t>(per, p.J - jc), rows = (int)min<int64_t>(16 * NI, i1 - i0);
 #pragma unroll 1
@@ -473,7 +485,7 @@ __global__ __launch_bounds__(64) void product_join_kernel(ProductArgs p, int par
 #pragma unroll
         for (int b = 0; b < NJ; ++b) acc[0][b] += from[b * 64];
     }
-    store_tile<SCALE, 1, NJ>(p, acc, t.g, t.yoff, t.i0 + wave % 2 * 64 + a * 16, t.i1,
+    store_tile<SCALE, 1, NJ, false>(p, acc, t.g, t.yoff, t.i0 + wave % 2 * 64 + a * 16, t.i1,
                              (int64_t)t.tj * BJ + wave / 2 * 64, lane, lds);
 }
 
@@ -592,7 +604,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void product_kernel(ProductArgs p) {
     // every wave is done with the operands' buffers, which now carry the results
     static_assert(512 * NI * NJ * WI * WJ <= (int)sizeof(lds), "the results of each wave");
     __syncthreads();
-    store_tile<SCALE, NI, NJ>(p, acc, g, yoff, i0 + wi * (BI / WI), i1, j0 + wj * (BJ / WJ), lane,
+    store_tile<SCALE, NI, NJ, false>(p, acc, g, yoff, i0 + wi * (BI / WI), i1, j0 + wj * (BJ / WJ), lane,
                               lds + wave * 512 * NI * NJ);
 }
 
@@ -618,8 +630,8 @@ __device__ __forceinline__ void stage_wait() {
 
 // The same product for operands whose rows begin on 16 bytes and whose widths are
 // whole 16-byte chunks: each step's tiles go straight from memory to LDS, into the
-// other of two buffers while a step is computed.
-template <int ET, int MODE, int SCALE, int BI, int BJ, int WI, int WJ>
+// others of NB buffers while a step is computed.
+template <int ET, int MODE, int SCALE, int BI, int BJ, int WI, int WJ, int NB = 2>
 __global__ __launch_bounds__(64 * WI * WJ) void product_direct_kernel(ProductArgs p) {
     constexpr bool PS = MODE == GRAD_W, QS = MODE != FWD;
     typedef Tile<ET, PS, BI> TP;
@@ -628,7 +640,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void product_direct_kernel(ProductArg
     constexpr int NTH = 64 * WI * WJ, CP = TP::CHUNKS / NTH, CQ = TQ::CHUNKS / NTH;
     constexpr int NI = BI / WI / 16, NJ = BJ / WJ / 16;
     constexpr int BUF = TP::BYTES + TQ::BYTES;
-    __shared__ __align__(1024) char lds[2 * BUF];
+    __shared__ __align__(1024) char lds[NB * BUF];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wi = wave % WI, wj = wave / WI;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
@@ -799,13 +811,13 @@ __global__ __launch_bounds__(64 * WI * WJ) void product_direct_kernel(ProductArg
             // products begin: the second half's are read during the first, the next
             // step's first during the second.  The barrier between the halves says that
             // the step's buffer has been read, so the second half also issues the loads
-            // of the step after next, which have a step's time.
+            // of step s + NB, which have NB - 1 steps' time.
             constexpr int ALL = NI * NJ, READS = NI + NJ;
             static_assert(2 * READS <= ALL && ALL % LOADS == 0, "room between the products");
             intx4 fp[2][NI], fq[2][NJ];
             // operand i of half h of step s, in the order of use
             auto read = [&](int s, int h, int i) {
-                const char *lp = lds + (s & 1) * BUF;
+                const char *lp = lds + (s & (NB - 1)) * BUF;
                 if (i == 0 || i > NI)
                     fq[h][i ? i - NI : 0] = TQ::read(lp + TP::BYTES, jq + (i ? i - NI : 0) * 16, h, lane);
                 else
@@ -821,17 +833,24 @@ __global__ __launch_bounds__(64 * WI * WJ) void product_direct_kernel(ProductArg
                         __builtin_amdgcn_sched_barrier(0);
                     }
                     mfma_in_place<ET>(fq[h][b], fp[h][a], acc[a][b]);
-                    if (h == 1 && n % (ALL / LOADS) == 1 && (main || s + 2 < steps))
-                        load(s + 2, s & 1, n / (ALL / LOADS), main);
+                    if (h == 1 && n % (ALL / LOADS) == 1 && (main || s + NB < steps))
+                        load(s + NB, s & (NB - 1), n / (ALL / LOADS), main);
                 }
             };
-            stage(0, 0);
-            if (steps > 1) {
-                stage(1, 1);
-                stage_wait<LOADS>();
-            } else {
-                stage_wait();
-            }
+            // of the `more` steps that were begun after the one that is waited for
+            auto wait = [&](int more) {
+                if (NB > 2 && more > 2)
+                    stage_wait<3 * LOADS>();
+                else if (NB > 2 && more == 2)
+                    stage_wait<2 * LOADS>();
+                else if (more == 1)
+                    stage_wait<LOADS>();
+                else
+                    stage_wait();
+            };
+            const int begun = min(NB, steps);
+            for (int s = 0; s < begun; ++s) stage(s, s);
+            wait(begun - 1);
 #pragma unroll
             for (int i = 0; i < READS; ++i) read(0, 0, i);
 #pragma unroll
@@ -840,14 +859,14 @@ __global__ __launch_bounds__(64 * WI * WJ) void product_direct_kernel(ProductArg
                 for (int b = 0; b < NJ; ++b) asm volatile("" : "+a"(acc[a][b]));
             settle();
             int s = 0;
-            for (; s + 2 < whole; ++s) {
+            for (; s + NB < whole; ++s) {
                 half(s, 0, true);
-                stage_wait();
+                stage_wait<(NB - 2) * LOADS>();
                 half(s, 1, true);
             }
             for (; s < steps; ++s) {
                 half(s, 0, false);
-                stage_wait();
+                wait(min(NB - 2, max(steps - 2 - s, 0)));
                 half(s, 1, false);
             }
             settle();
@@ -864,7 +883,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void product_direct_kernel(ProductArg
     // every wave is done with the operands' buffers, which now carry the results
     static_assert(512 * NI * NJ * WI * WJ <= (int)sizeof(lds), "the results of each wave");
     __syncthreads();
-    store_tile<SCALE, NI, NJ>(p, acc, g, yoff, i0 + wi * (BI / WI), i1, j0 + wj * (BJ / WJ), lane,
+    store_tile<SCALE, NI, NJ, BI == 256>(p, acc, g, yoff, i0 + wi * (BI / WI), i1, j0 + wj * (BJ / WJ), lane,
                               lds + wave * 512 * NI * NJ);
 }
 
@@ -1058,6 +1077,11 @@ void launch(ProductArgs &p, hipStream_t s) {
     if constexpr (MODE == FWD)
         if (few_rows(p.rows, p.groups, p.offsets != nullptr)) return launch_few<ET, SCALE>(p, s);
     constexpr int ES = ET == F8 ? 1 : 2;
+    // Small tiles have 4 buffers where a CU gets one workgroup, as in the tail: loads have
+    // 3 steps' time (gradients of 8192 rows by 16 groups of 4096 x 2048: 344 against 353
+    // us, of 1003 by 24 of 1000 x 520: 31.4 against 33.5).  In the fp8 form the compiler's
+    // own waits for the scales would wait for these loads too.
+    constexpr int NB = ET == F8 ? 2 : 4;
     // whole 16-byte chunks everywhere, and offsets inside a tile in 32 bits
     bool direct = aligned(p.P, 16) && aligned(p.Q, 16) && p.ldp % 16 == 0 && p.ldq % 16 == 0 &&
                   p.group_q % 16 == 0 && p.ldp < (1 << 22) && p.ldq < (1 << 22);
@@ -1080,15 +1104,19 @@ void launch(ProductArgs &p, hipStream_t s) {
                            dim3(128 * WI), 0, s, p);
         if (p.tail) {
             p.tail = 2;
-            hipLaunchKernelGGL((product_direct_kernel<ET, MODE, SCALE, 128, 128, 2, 2>), dim3(4 * 128), dim3(256), 0, s, p);
+            hipLaunchKernelGGL((product_direct_kernel<ET, MODE, SCALE, 128, 128, 2, 2, NB>), dim3(4 * 128), dim3(256), 0, s, p);
         }
         return;
     }
     const unsigned grid = grid_of<MODE, 128, 128>(p);
     if (direct) {
         p.splits = splits;
-        hipLaunchKernelGGL((product_direct_kernel<ET, MODE, SCALE, 128, 128, 2, 2>), dim3(grid * splits), dim3(256),
-                           0, s, p);
+        if (grid * splits <= 256)
+            hipLaunchKernelGGL((product_direct_kernel<ET, MODE, SCALE, 128, 128, 2, 2, NB>), dim3(grid * splits),
+                               dim3(256), 0, s, p);
+        else
+            hipLaunchKernelGGL((product_direct_kernel<ET, MODE, SCALE, 128, 128, 2, 2>), dim3(grid * splits), dim3(256),
+                               0, s, p);
     } else {
         p.splits = splits;
         hipLaunchKernelGGL((product_kernel<ET, MODE, SCALE, 128, 128, 2, 2>), dim3(grid * splits), dim3(256), 0, s, p);
