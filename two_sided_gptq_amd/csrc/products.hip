@@ -47,7 +47,8 @@ struct ProductArgs {
     int vec;                 // 1: rows of C start on 16 bytes
     int splits;              // parts of the reduction, each a workgroup of its own
     float *part;             // with splits > 1: the parts' sums, as the accumulators hold them
-    int tail;                // 1: large tiles but for the tail; 2: the tail, in small tiles
+    int tail;                // 1: large tiles leave their tail to small ones
+    unsigned large;          // workgroups of large tiles, before those of a tail in their launch
 };
 
 // A value that is the same in every lane, in a scalar register.
@@ -96,19 +97,20 @@ __device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t total) {
 }
 
 // How many of `total` large tiles a launch of them takes.  A last round that would use
-// half of the 256 CUs or less is left to a second launch, whose small tiles, four to a
-// large one, take two thirds of a round's time or less (bf16, 16384 rows by 8 groups of
+// half of the 256 CUs or less is left to small tiles, which, four to a large one, take
+// two thirds of a round's time or less (bf16, 16384 rows by 8 groups of
 // 11008 x 4096: 1.19 against 1.26 ms; 8192 x 4352 x 1024: 80 against 87 us).
 __host__ __device__ __forceinline__ int64_t without_tail(int64_t total) {
     const int64_t rem = total & 255;
     return total > 256 && rem <= 128 ? total - rem : total;
 }
+constexpr unsigned TAIL_MOST = 4 * 128;  // workgroups of a tail
 
 // Finds the workgroup's rows: tiles of BI rows are counted group by group, then
 // walked in bands of 8 row tiles.  All 64 lanes of a wave take part; the results are
 // wave uniform.  False: no work for this workgroup.
 template <int BI>
-__device__ __forceinline__ bool find_rows(const ProductArgs &p, int64_t b, int &g, int64_t &i0, int64_t &i1,
+__device__ __forceinline__ bool find_rows(const ProductArgs &p, int64_t b, bool tail, int &g, int64_t &i0, int64_t &i1,
                                           int &tj, int64_t &w) {
     const int lane = threadIdx.x & 63;
     // lane e holds group e's first row and tiles, for the first 64 groups
@@ -130,7 +132,7 @@ __device__ __forceinline__ bool find_rows(const ProductArgs &p, int64_t b, int &
             slots += __builtin_amdgcn_readlane(wave_scan(tiles_of(base + lane)), 63);
     }
     const int64_t total = (int64_t)slots * p.tiles_j, most = p.tail ? without_tail(total) : total;
-    if (p.tail == 2) {
+    if (tail) {
         w = most + b;
         if (w >= total) return false;
     } else {
@@ -180,20 +182,19 @@ struct Work {
 };
 
 template <int MODE, int BI, int KR>
-__device__ __forceinline__ bool find_work(const ProductArgs &p, Work &t) {
+__device__ __forceinline__ bool find_work(const ProductArgs &p, unsigned block, bool tail, Work &t) {
     report_offsets(p);
     // in the tail, four workgroups of one XCD share a large tile
     constexpr int LARGE = 256;
-    const bool tail = BI < LARGE && p.tail == 2;
-    const int64_t b = tail ? (blockIdx.x >> 5 << 3) + (blockIdx.x & 7) : blockIdx.x / p.splits;
-    const int part = tail ? 0 : blockIdx.x % p.splits, quarter = tail ? blockIdx.x >> 3 & 3 : 0;
+    const int64_t b = tail ? (block >> 5 << 3) + (block & 7) : block / p.splits;
+    const int part = tail ? 0 : block % p.splits, quarter = tail ? block >> 3 & 3 : 0;
     const int size = tail ? LARGE : BI;
     t.P = p.P, t.Q = p.Q, t.R = p.R, t.yoff = 0;
     int64_t w;
     if constexpr (MODE == GRAD_W) {
         const int64_t tiles = (int64_t)p.tiles_i * p.tiles_j, total = tiles * p.groups;
-        const int64_t most = p.tail ? without_tail(total) : total, at = p.tail == 2 ? most + b : b;
-        if (at >= (p.tail == 2 ? total : most)) return false;
+        const int64_t most = p.tail ? without_tail(total) : total, at = tail ? most + b : b;
+        if (at >= (tail ? total : most)) return false;
         // every XCD gets a part of each group's tiles: groups differ in length (8192 rows
         // in 16 uneven groups, both gradients: 0.41 against 0.45 ms)
         t.g = (int)(at / tiles);
@@ -214,7 +215,8 @@ __device__ __forceinline__ bool find_work(const ProductArgs &p, Work &t) {
         t.Q += a * p.ldq;
         t.yoff = t.g * p.group_y;
     } else {
-        if (tail ? !find_rows<LARGE>(p, b, t.g, t.i0, t.i1, t.tj, w) : !find_rows<BI>(p, b, t.g, t.i0, t.i1, t.tj, w))
+        if (tail ? !find_rows<LARGE>(p, b, true, t.g, t.i0, t.i1, t.tj, w)
+                 : !find_rows<BI>(p, b, false, t.g, t.i0, t.i1, t.tj, w))
             return false;
         t.g = (int)uniform(t.g), t.tj = (int)uniform(t.tj);
         t.i0 = uniform(t.i0), t.i1 = uniform(t.i1);
@@ -471,7 +473,7 @@ __global__ __launch_bounds__(64) void product_join_kernel(ProductArgs p, int par
     const int lane = threadIdx.x;
     Work t;
     p.splits = PIECES;
-    if (!find_work<MODE, BI, KR>(p, t)) return;
+    if (!find_work<MODE, BI, KR>(p, blockIdx.x, false, t)) return;
     const int64_t tile = t.nth / PIECES;
     const int piece = (int)(t.nth % PIECES), wave = piece / NI, a = piece % NI;
     floatx4 acc[1][NJ];
@@ -506,7 +508,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void product_kernel(ProductArgs p) {
     const int wi = wave % WI, wj = wave / WI;
 
     Work t;
-    if (!find_work<MODE, BI, KR>(p, t)) return;
+    if (!find_work<MODE, BI, KR>(p, blockIdx.x, false, t)) return;
     const int g = t.g;
     const int64_t i0 = t.i0, i1 = t.i1, j0 = (int64_t)t.tj * BJ, R = t.R, yoff = t.yoff;
     const char *P = t.P, *Q = t.Q;
@@ -631,8 +633,9 @@ __device__ __forceinline__ void stage_wait() {
 // The same product for operands whose rows begin on 16 bytes and whose widths are
 // whole 16-byte chunks: each step's tiles go straight from memory to LDS, into the
 // others of NB buffers while a step is computed.
-template <int ET, int MODE, int SCALE, int BI, int BJ, int WI, int WJ, int NB = 2>
-__global__ __launch_bounds__(64 * WI * WJ) void product_direct_kernel(ProductArgs p) {
+// `lds` holds NB steps of both operands.
+template <int ET, int MODE, int SCALE, int BI, int BJ, int WI, int WJ, int NB>
+__device__ __forceinline__ void direct_tile(const ProductArgs &p, unsigned block, bool tail, char *lds) {
     constexpr bool PS = MODE == GRAD_W, QS = MODE != FWD;
     typedef Tile<ET, PS, BI> TP;
     typedef Tile<ET, QS, BJ> TQ;
@@ -640,13 +643,12 @@ __global__ __launch_bounds__(64 * WI * WJ) void product_direct_kernel(ProductArg
     constexpr int NTH = 64 * WI * WJ, CP = TP::CHUNKS / NTH, CQ = TQ::CHUNKS / NTH;
     constexpr int NI = BI / WI / 16, NJ = BJ / WJ / 16;
     constexpr int BUF = TP::BYTES + TQ::BYTES;
-    __shared__ __align__(1024) char lds[NB * BUF];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wi = wave % WI, wj = wave / WI;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
 
     Work t;
-    if (!find_work<MODE, BI, KR>(p, t)) return;
+    if (!find_work<MODE, BI, KR>(p, block, tail, t)) return;
     const int g = t.g;
     const int64_t i0 = t.i0, i1 = t.i1, j0 = (int64_t)t.tj * BJ, R = t.R, yoff = t.yoff;
     const char *P = t.P, *Q = t.Q;
@@ -881,10 +883,36 @@ __global__ __launch_bounds__(64 * WI * WJ) void product_direct_kernel(ProductArg
         return;
     }
     // every wave is done with the operands' buffers, which now carry the results
-    static_assert(512 * NI * NJ * WI * WJ <= (int)sizeof(lds), "the results of each wave");
+    static_assert(512 * NI * NJ * WI * WJ <= NB * BUF, "the results of each wave");
     __syncthreads();
     store_tile<SCALE, NI, NJ, BI == 256>(p, acc, g, yoff, i0 + wi * (BI / WI), i1, j0 + wj * (BJ / WJ), lane,
                               lds + wave * 512 * NI * NJ);
+}
+
+template <int ET, int MODE, int SCALE, int NB, bool TAIL>
+__global__ __launch_bounds__(256) void product_direct_kernel(ProductArgs p) {
+    __shared__ __align__(1024) char lds[NB * 256 * STEP];
+    direct_tile<ET, MODE, SCALE, 128, 128, 2, 2, NB>(p, blockIdx.x, TAIL, lds);
+}
+
+// 4 waves hold 128 x 128 accumulators each: a third less of LDS reads than 8 waves of
+// 64 x 128 (bf16 8192 x 8192 x 8192 0.754 against 0.797 ms).  fp8 sums are added by
+// vector instructions, which cannot use the registers that 4 waves need.
+constexpr int large_waves(int et) { return et == F8 ? 8 : 4; }
+
+// Large tiles; of 16-bit types, then their tail in small ones, which begins where the
+// first CUs fall idle (bf16, 16384 rows by 8 groups of 11008 x 4096: 1.17 against 1.19
+// ms as a second launch; 8192 x 4352 x 1024: 73 against 77 us).  fp8 tails gain from two
+// workgroups on a CU instead, which the LDS of a large tile rules out (12000 rows by 16
+// groups of 4096 x 2048: 133 us as a second launch, 141 here).
+template <int ET, int MODE, int SCALE>
+__global__ __launch_bounds__(64 * large_waves(ET)) void product_large_kernel(ProductArgs p) {
+    constexpr int WI = large_waves(ET) / 2;
+    __shared__ __align__(1024) char lds[2 * 512 * STEP];
+    if (ET == F8 || blockIdx.x < p.large)
+        direct_tile<ET, MODE, SCALE, 256, 256, WI, 2, 2>(p, blockIdx.x, false, lds);
+    else if constexpr (ET != F8)
+        direct_tile<ET, MODE, SCALE, 128, 128, WI, 2, 4>(p, blockIdx.x - p.large, true, lds);
 }
 
 // Few rows a group (decoding): the weights stream past once and bound the time, so
@@ -903,7 +931,7 @@ __global__ __launch_bounds__(1024) void product_few_kernel(ProductArgs p, int wn
     report_offsets(p);
     int g, tj;
     int64_t i0, i1, nth;
-    if (!find_rows<16>(p, blockIdx.x, g, i0, i1, tj, nth)) return;
+    if (!find_rows<16>(p, blockIdx.x, false, g, i0, i1, tj, nth)) return;
     g = (int)uniform(g), tj = (int)uniform(tj);
     i0 = uniform(i0), i1 = uniform(i1);
     const int64_t j0 = (int64_t)tj * 16 * wn + wave % wn * 16;
@@ -1077,11 +1105,6 @@ void launch(ProductArgs &p, hipStream_t s) {
     if constexpr (MODE == FWD)
         if (few_rows(p.rows, p.groups, p.offsets != nullptr)) return launch_few<ET, SCALE>(p, s);
     constexpr int ES = ET == F8 ? 1 : 2;
-    // Small tiles have 4 buffers where a CU gets one workgroup, as in the tail: loads have
-    // 3 steps' time (gradients of 8192 rows by 16 groups of 4096 x 2048: 344 against 353
-    // us, of 1003 by 24 of 1000 x 520: 31.4 against 33.5).  In the fp8 form the compiler's
-    // own waits for the scales would wait for these loads too.
-    constexpr int NB = ET == F8 ? 2 : 4;
     // whole 16-byte chunks everywhere, and offsets inside a tile in 32 bits
     bool direct = aligned(p.P, 16) && aligned(p.Q, 16) && p.ldp % 16 == 0 && p.ldq % 16 == 0 &&
                   p.group_q % 16 == 0 && p.ldp < (1 << 22) && p.ldq < (1 << 22);
@@ -1093,32 +1116,32 @@ void launch(ProductArgs &p, hipStream_t s) {
         splits = choose_splits(MODE, p.rows, p.I, p.J, steps_of(MODE, ES, p.rows, p.R, p.groups), p.groups, p.offsets != nullptr);
     }
     if (direct && large_tiles(MODE, p.rows, p.I, p.J, p.groups, p.offsets != nullptr)) {
-        // 4 waves hold 128 x 128 accumulators each: a third less of LDS reads than 8 waves
-        // of 64 x 128 (bf16 8192 x 8192 x 8192 0.754 against 0.797 ms).  fp8 sums are added
-        // by vector instructions, which cannot use the registers that 4 waves need.
-        constexpr int WI = ET == F8 ? 4 : 2;
         const unsigned grid = grid_of<MODE, 256, 256>(p);
-        // with groups of rows only the device knows how many tiles there are
+        // With groups of rows only the device knows how many tiles there are.
         p.tail = MODE != GRAD_W && p.offsets ? grid > 256 : without_tail(grid) < grid;
-        hipLaunchKernelGGL((product_direct_kernel<ET, MODE, SCALE, 256, 256, WI, 2>), dim3(grid),
-                           dim3(128 * WI), 0, s, p);
-        if (p.tail) {
-            p.tail = 2;
-            hipLaunchKernelGGL((product_direct_kernel<ET, MODE, SCALE, 128, 128, 2, 2, NB>), dim3(4 * 128), dim3(256), 0, s, p);
-        }
+        p.large = (grid + 7) & ~7u;  // the tail's first workgroup goes to XCD 0
+        hipLaunchKernelGGL((product_large_kernel<ET, MODE, SCALE>), dim3(p.large + (p.tail && ET != F8 ? TAIL_MOST : 0)),
+                           dim3(64 * large_waves(ET)), 0, s, p);
+        if constexpr (ET == F8)
+            if (p.tail)
+                hipLaunchKernelGGL((product_direct_kernel<ET, MODE, SCALE, 2, true>), dim3(TAIL_MOST), dim3(256), 0, s, p);
         return;
     }
     const unsigned grid = grid_of<MODE, 128, 128>(p);
+    p.splits = splits;
     if (direct) {
-        p.splits = splits;
+        // 4 buffers where a CU gets one workgroup, as in the tail: loads have 3 steps' time
+        // (gradients of 8192 rows by 16 groups of 4096 x 2048: 344 against 353 us, of 1003
+        // by 24 of 1000 x 520: 31.4 against 33.5).  In the fp8 form the compiler's own
+        // waits for the scales would wait for these loads too.
+        constexpr int NB = ET == F8 ? 2 : 4;
         if (grid * splits <= 256)
-            hipLaunchKernelGGL((product_direct_kernel<ET, MODE, SCALE, 128, 128, 2, 2, NB>), dim3(grid * splits),
-                               dim3(256), 0, s, p);
+            hipLaunchKernelGGL((product_direct_kernel<ET, MODE, SCALE, NB, false>), dim3(grid * splits), dim3(256), 0,
+                               s, p);
         else
-            hipLaunchKernelGGL((product_direct_kernel<ET, MODE, SCALE, 128, 128, 2, 2>), dim3(grid * splits), dim3(256),
-                               0, s, p);
+            hipLaunchKernelGGL((product_direct_kernel<ET, MODE, SCALE, 2, false>), dim3(grid * splits), dim3(256), 0,
+                               s, p);
     } else {
-        p.splits = splits;
         hipLaunchKernelGGL((product_kernel<ET, MODE, SCALE, 128, 128, 2, 2>), dim3(grid * splits), dim3(256), 0, s, p);
     }
     if (splits > 1) {
