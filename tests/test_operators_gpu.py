@@ -165,6 +165,8 @@ FP8_CASES = [
     # few rows: the form for single tokens, its widths and ends
     (1, 4096, 1040, 1, "block", "bf16", 0), (2, 40, 2500, 1, "row", "f16", 1), (20, 1000, 384, 1, "block", "bf16", 0),
     (50, 333, 640, 1, "row", "bf16", 0), (64, 512, 129, 1, "block", "f16", 0), (30, 272, 400, 16, "row", "bf16", 0),
+    # and rows that begin off whole dwords
+    (3, 200, 3077, 1, "row", "bf16", 0), (9, 130, 1500, 5, "block", "f16", 2), (1, 90, 2999, 1, "block", "bf16", 3),
     (150, 100, 256, 9, "block", "bf16", 0),
     # few tiles and a long reduction, which is split
     (40, 260, 4200, 1, "block", "bf16", 0), (130, 100, 6416, 1, "row", "f16", 0), (200, 130, 4112, 3, "block", "bf16", 0)]
@@ -229,6 +231,7 @@ GROUPED_CASES = [
     (400, 2616, 2632, 3, "bf16", None, 0, 0),
     # few rows
     (1, 300, 1000, 1, "bf16", None, 0, 0), (2, 33, 2050, 1, "f16", "f32", 1, 1), (60, 1000, 200, 1, "bf16", None, 0, 0),
+    (3, 130, 3077, 1, "bf16", None, 0, 1), (40, 70, 1111, 20, "f16", None, 2, 3), (1, 48, 2304, 1, "bf16", "f32", 1, 0),
     (90, 130, 520, 7, "bf16", "f32", 0, 0), (33, 272, 264, 40, "f16", None, 0, 0),
     # few tiles and a long reduction, which is split: forward, gradients
     (300, 136, 2104, 3, "bf16", None, 0, 0), (100, 2201, 130, 2, "f16", "f32", 0, 0), (6000, 130, 70, 2, "bf16", "f32", 0, 0),

@@ -99,7 +99,8 @@ __device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t total) {
 // How many of `total` large tiles a launch of them takes.  A last round that would use
 // half of the 256 CUs or less is left to small tiles, which, four to a large one, take
 // two thirds of a round's time or less (bf16, 16384 rows by 8 groups of
-// 11008 x 4096: 1.19 against 1.26 ms; 8192 x 4352 x 1024: 80 against 87 us).
+// 11008 x 4096: 1.19 against 1.26 ms; 8192 x 2816 x 4096, 96 tiles left: 162 against
+// 166 us).  With more left they do not (8192 x 3328 x 4096, 160 left: 188 against 174).
 __host__ __device__ __forceinline__ int64_t without_tail(int64_t total) {
     const int64_t rem = total & 255;
     return total > 256 && rem <= 128 ? total - rem : total;
@@ -920,8 +921,24 @@ __global__ __launch_bounds__(64 * large_waves(ET)) void product_large_kernel(Pro
 // rows of X; the waves of a workgroup are wn sets of rows by wk parts of the
 // reduction, which is dealt out in blocks of 128 bytes.  The parts' sums are added in
 // a fixed order in LDS.  UNROLL blocks of both operands are loaded before the first is
-// multiplied.
-template <int ET, int SCALE>
+// multiplied.  Loads that are not on whole dwords take three times as long (bf16, 4 rows
+// by 4096 x 14337: 68 us, 28 at 14338 columns), so with ODD rows the dwords around
+// a chunk are loaded and shifted (38 us).
+__device__ __forceinline__ intx4 shifted(const intx4 &v, int next, uint32_t bytes) {
+    intx4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r[i] = (int)__builtin_amdgcn_alignbyte((uint32_t)(i < 3 ? v[i < 3 ? i + 1 : 3] : next), (uint32_t)v[i], bytes);
+    return r;
+}
+// 16 bytes from src's dword on, and the dword of src's 16th byte: no byte outside dwords
+// that hold some of the 16 is read.
+__device__ __forceinline__ void load_around(const char *src, intx4 &v, int &next) {
+    const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(src) & 3;
+    __builtin_memcpy(&v, __builtin_assume_aligned(src - off, 4), 16);
+    __builtin_memcpy(&next, __builtin_assume_aligned(src - off + (off ? 16 : 12), 4), 4);
+}
+template <int ET, int SCALE, bool ODD>
 __global__ __launch_bounds__(1024) void product_few_kernel(ProductArgs p, int wn) {
     constexpr int ES = ET == F8 ? 1 : 2, KR = STEP / ES, EC = 16 / ES, UNROLL = 4;
     extern __shared__ __align__(16) char lds[];
@@ -946,6 +963,7 @@ __global__ __launch_bounds__(1024) void product_few_kernel(ProductArgs p, int wn
 
     for (int b0 = kpart; b0 < blocks; b0 += UNROLL * wk) {
         intx4 fw[UNROLL][2], fx[UNROLL][2];
+        int nw[UNROLL][2], nx[UNROLL][2];
         float sc[UNROLL];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
@@ -955,12 +973,18 @@ __global__ __launch_bounds__(1024) void product_few_kernel(ProductArgs p, int wn
             if (left >= KR) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    __builtin_memcpy(&fw[u][h], w + at + 64 * h, 16);
-                    __builtin_memcpy(&fx[u][h], x + at + 64 * h, 16);
+                    if constexpr (ODD) {
+                        load_around(w + at + 64 * h, fw[u][h], nw[u][h]);
+                        load_around(x + at + 64 * h, fx[u][h], nx[u][h]);
+                    } else {
+                        __builtin_memcpy(&fw[u][h], w + at + 64 * h, 16);
+                        __builtin_memcpy(&fx[u][h], x + at + 64 * h, 16);
+                    }
                 }
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    nw[u][h] = nx[u][h] = 0;
                     fw[u][h] = chunk<ES>(w + at + 64 * h, left - (4 * h + q) * EC);
                     fx[u][h] = chunk<ES>(x + at + 64 * h, left - (4 * h + q) * EC);
                 }
@@ -973,6 +997,16 @@ __global__ __launch_bounds__(1024) void product_few_kernel(ProductArgs p, int wn
         }
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
+            if constexpr (ODD) {
+                const bool shift = b0 + u * wk < p.R / KR;
+                const uint32_t bw = shift ? (uint32_t)reinterpret_cast<uintptr_t>(w) & 3 : 0;
+                const uint32_t bx = shift ? (uint32_t)reinterpret_cast<uintptr_t>(x) & 3 : 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    fw[u][h] = shifted(fw[u][h], nw[u][h], bw);
+                    fx[u][h] = shifted(fx[u][h], nx[u][h], bx);
+                }
+            }
             if constexpr (ET == F8) {
                 const floatx4 s = mfma_f8(fw[u][0], fw[u][1], fx[u][0], fx[u][1]);
 #pragma unroll
@@ -1096,8 +1130,11 @@ void launch_few(ProductArgs &p, hipStream_t s) {
     const int wn = wk >= 4 ? 1 : 4 / wk;
     p.tiles_j = (int)((p.J + 16 * wn - 1) / (16 * wn));
     const int64_t grid = ((p.rows + 15) / 16 + (p.offsets ? p.groups + 1 : 0)) * p.tiles_j;
-    hipLaunchKernelGGL((product_few_kernel<ET, SCALE>), dim3((unsigned)grid), dim3(64 * wn * wk),
-                       wk > 1 ? wn * wk * 1024 : 0, s, p, wn);
+    const unsigned part = wk > 1 ? wn * wk * 1024 : 0;
+    if (aligned(p.P, 4) && aligned(p.Q, 4) && p.ldp % 4 == 0 && p.ldq % 4 == 0)
+        hipLaunchKernelGGL((product_few_kernel<ET, SCALE, false>), dim3((unsigned)grid), dim3(64 * wn * wk), part, s, p, wn);
+    else
+        hipLaunchKernelGGL((product_few_kernel<ET, SCALE, true>), dim3((unsigned)grid), dim3(64 * wn * wk), part, s, p, wn);
 }
 
 template <int ET, int MODE, int SCALE>
