@@ -13,6 +13,7 @@
 
 #include "common.hpp"
 #include "elem.hpp"
+#include "walk.hpp"
 
 namespace bakron {
 namespace {
@@ -44,6 +45,7 @@ struct ProductArgs {
     int32_t *dev_status;
     int ytype;
     int tiles_i, tiles_j;    // tiles_i: gradient W
+    int slots;               // row tiles that launch and workspace are sized for (forward, gradient X)
     int vec;                 // 1: rows of C start on 16 bytes
     int splits;              // parts of the reduction, each a workgroup of its own
     float *part;             // with splits > 1: the parts' sums, as the accumulators hold them
@@ -66,16 +68,8 @@ __device__ __forceinline__ int wave_scan(int x) {
     return x;
 }
 
-// Group g's rows [a, b), kept inside [0, rows) whatever the offsets hold.  Group
-// `groups` stands for the rows after the last group.
 __device__ __forceinline__ void group_range(const ProductArgs &p, int g, int64_t &a, int64_t &b) {
-    if (!p.offsets) {
-        a = g == 0 ? 0 : p.rows;
-        b = p.rows;
-        return;
-    }
-    a = g == 0 ? 0 : min<int64_t>(max<int64_t>(p.offsets[g], 0), p.rows);
-    b = g == p.groups ? p.rows : min<int64_t>(max<int64_t>(p.offsets[g + 1], a), p.rows);
+    rows_of_group(p.offsets, p.groups, p.rows, g, a, b);
 }
 
 // Offsets that fall or leave [0, rows] are reported once.
@@ -89,23 +83,7 @@ __device__ __forceinline__ void report_offsets(const ProductArgs &p) {
     if (bad) atomicOr(p.dev_status, BAKRON_DEV_BAD_INDEX);
 }
 
-// Workgroups are dealt to the 8 XCDs in turn: XCD x takes the x-th eighth of the
-// work, so that tiles that share operands share an L2.
-__device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t total) {
-    const int64_t q = total >> 3, r = total & 7, x = b & 7;
-    return x * q + min(x, r) + (b >> 3);
-}
-
-// How many of `total` large tiles a launch of them takes.  A last round that would use
-// half of the 256 CUs or less is left to small tiles, which, four to a large one, take
-// two thirds of a round's time or less (bf16, 16384 rows by 8 groups of
-// 11008 x 4096: 1.19 against 1.26 ms; 8192 x 2816 x 4096, 96 tiles left: 162 against
-// 166 us).  With more left they do not (8192 x 3328 x 4096, 160 left: 188 against 174).
-__host__ __device__ __forceinline__ int64_t without_tail(int64_t total) {
-    const int64_t rem = total & 255;
-    return total > 256 && rem <= 128 ? total - rem : total;
-}
-constexpr unsigned TAIL_MOST = 4 * 128;  // workgroups of a tail
+constexpr unsigned TAIL_MOST = 4 * 128;  // workgroups of a tail (without_tail)
 
 // Finds the workgroup's rows: tiles of BI rows are counted group by group, then
 // walked in bands of 8 row tiles.  All 64 lanes of a wave take part; the results are
@@ -132,19 +110,9 @@ __device__ __forceinline__ bool find_rows(const ProductArgs &p, int64_t b, bool 
         for (int base = 64; base <= p.groups; base += 64)
             slots += __builtin_amdgcn_readlane(wave_scan(tiles_of(base + lane)), 63);
     }
-    const int64_t total = (int64_t)slots * p.tiles_j, most = p.tail ? without_tail(total) : total;
-    if (tail) {
-        w = most + b;
-        if (w >= total) return false;
-    } else {
-        if (b >= most) return false;
-        w = xcd_order(b, most);
-    }
-    const int64_t per_band = 8 * (int64_t)p.tiles_j;
-    const int64_t band = w / per_band, in = w - band * per_band;
-    const int width = (int)min<int64_t>(8, slots - band * 8);
-    int slot = (int)(band * 8) + (int)in % width;
-    tj = (int)uniform((int)in / width);
+    int slot;
+    if (!place_of(slots, p.slots, p.tiles_j, p.tail, tail, b, w, slot, tj)) return false;
+    tj = (int)uniform(tj);
     slot = (int)uniform(slot);
     if (!p.offsets) {
         g = 0;
@@ -1051,7 +1019,8 @@ unsigned grid_of(ProductArgs &p) {
     p.tiles_j = (int)((p.J + BJ - 1) / BJ);
     p.tiles_i = (int)((p.I + BI - 1) / BI);
     if (MODE == GRAD_W) return (unsigned)((int64_t)p.groups * p.tiles_i * p.tiles_j);
-    return (unsigned)(((p.rows + BI - 1) / BI + (p.offsets ? p.groups + 1 : 0)) * p.tiles_j);
+    p.slots = (int)row_tiles(BI, p.rows, p.groups, p.offsets != nullptr);
+    return (unsigned)((int64_t)p.slots * p.tiles_j);
 }
 
 // Tiles of b x b that a launch has, about: a group's last tile is half full on average,
@@ -1084,7 +1053,7 @@ bool large_tiles(int mode, int64_t rows, int64_t I, int64_t J, int groups, bool 
 int choose_splits(int mode, int64_t rows, int64_t I, int64_t J, int64_t steps, int groups, bool grouped) {
     if (large_tiles(mode, rows, I, J, groups, grouped)) return 1;
     const int64_t tiles = count_tiles(mode, 128, rows, I, J, groups, grouped);
-    const int64_t most = mode == GRAD_W ? tiles : ((rows + 127) / 128 + (grouped ? groups + 1 : 0)) * ((J + 127) / 128);
+    const int64_t most = mode == GRAD_W ? tiles : row_tiles(128, rows, groups, grouped) * ((J + 127) / 128);
     int best = 1;
     double least = 1e30;
     for (int s = 1; s <= 16 && s * 2 <= steps; s *= 2) {
@@ -1113,8 +1082,7 @@ size_t parts_size(int mode, int es, int64_t rows, int64_t I, int64_t J, int64_t 
     const int s = choose_splits(mode, rows, I, J, steps_of(mode, es, rows, R, groups), groups, grouped);
     if (s == 1) return 0;
     const int64_t tj = (J + 127) / 128;
-    const int64_t tiles = mode == GRAD_W ? groups * ((I + 127) / 128) * tj
-                                         : ((rows + 127) / 128 + (grouped ? groups + 1 : 0)) * tj;
+    const int64_t tiles = mode == GRAD_W ? groups * ((I + 127) / 128) * tj : row_tiles(128, rows, groups, grouped) * tj;
     return (size_t)(tiles * s) * 128 * 128 * sizeof(float);
 }
 
@@ -1129,7 +1097,8 @@ void launch_few(ProductArgs &p, hipStream_t s) {
     while (wk < 16 && wk * 2 * sets <= 4096 && wk * 2 <= blocks) wk *= 2;
     const int wn = wk >= 4 ? 1 : 4 / wk;
     p.tiles_j = (int)((p.J + 16 * wn - 1) / (16 * wn));
-    const int64_t grid = ((p.rows + 15) / 16 + (p.offsets ? p.groups + 1 : 0)) * p.tiles_j;
+    p.slots = (int)row_tiles(16, p.rows, p.groups, p.offsets != nullptr);
+    const int64_t grid = (int64_t)p.slots * p.tiles_j;
     const unsigned part = wk > 1 ? wn * wk * 1024 : 0;
     if (aligned(p.P, 4) && aligned(p.Q, 4) && p.ldp % 4 == 0 && p.ldq % 4 == 0)
         hipLaunchKernelGGL((product_few_kernel<ET, SCALE, false>), dim3((unsigned)grid), dim3(64 * wn * wk), part, s, p, wn);
