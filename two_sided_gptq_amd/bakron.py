@@ -306,6 +306,8 @@ def last_phase_ms() -> dict:
 
 # Operators for rounded layers.  Matrices are GPU tensors whose rows may lie apart
 # (a row's elements are adjacent); nothing is copied to make them contiguous.
+# `stream`: where the call runs, by default torch's current stream; inputs and given
+# outputs have to be ready for it.
 
 _TYPES = {torch.float32: T_F32, torch.bfloat16: T_BF16, torch.float16: T_F16}
 _FP8 = torch.float8_e4m3fn
@@ -345,16 +347,26 @@ def _out(out, shape, dtype, device, name):
     return out, _rows_of(out, name, (dtype,), len(shape))
 
 
-def _where(stream, *tensors):
-    """The stream's handle.  What this module allocated and hands to a stream other
-    than torch's current one is marked as used there."""
-    current = torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    if stream is None or stream.cuda_stream == current:
-        return current
-    for t in tensors:
+def _here():
+    """The handle of torch's current stream."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _elsewhere(stream):
+    return stream is not None and stream.cuda_stream != _here()
+
+
+def _on(stream, op, *args):
+    """op(*args) with `stream` as torch's current one, so that outputs and workspaces come
+    from its memory: what other streams still do there is over, or ordered before it.
+    The results are marked as used on the caller's stream, which frees them."""
+    caller = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        result = op(*args)
+    for t in result.values() if isinstance(result, dict) else result if isinstance(result, tuple) else (result,):
         if t is not None:
-            t.record_stream(stream)
-    return stream.cuda_stream
+            t.record_stream(caller)
+    return result
 
 
 def _status(t):
@@ -365,6 +377,8 @@ def fp8_quantize(X, block_rows=1, out=None, scales=None, dev_status=None, stream
     """X in e4m3 with a scale for each row (block_rows 1) or 128 rows (128) and 128
     columns (bakron_fp8_quantize).  Returns (codes as float8_e4m3fn, scales of
     shape (ceil(cols / 128), ceil(rows / block_rows)))."""
+    if _elsewhere(stream):
+        return _on(stream, fp8_quantize, X, block_rows, out, scales, dev_status)
     lib = load()
     ldx = _rows_of(X, "X", _TYPES)
     rows, cols = X.shape
@@ -375,12 +389,14 @@ def fp8_quantize(X, block_rows=1, out=None, scales=None, dev_status=None, stream
     S = torch.empty(of, dtype=torch.float32, device=X.device) if scales is None else scales
     sp = S.data_ptr() if scales is None else _vector(S, "scales", torch.float32, of)
     _check(lib.bakron_fp8_quantize(X.data_ptr(), _TYPES[X.dtype], rows, cols, ldx, block_rows, Q.data_ptr(),
-                                   ldq, sp, _status(dev_status), _where(stream, Q, S)), "bakron_fp8_quantize")
+                                   ldq, sp, _status(dev_status), _here()), "bakron_fp8_quantize")
     return Q, S
 
 
 def fp8_from_codes(codes, zeros=None, kind=Q_SYM, bits=4, out=None, stream=None):
     """The codes of a solve (2 to 4 bits) as e4m3 weights, exactly (bakron_fp8_from_codes)."""
+    if _elsewhere(stream):
+        return _on(stream, fp8_from_codes, codes, zeros, kind, bits, out)
     lib = load()
     if codes.dim() != 2 or codes.numel() == 0:
         raise BakronError(f"codes must have 2 dimensions, none of size 0, not {tuple(codes.shape)}")
@@ -388,7 +404,7 @@ def fp8_from_codes(codes, zeros=None, kind=Q_SYM, bits=4, out=None, stream=None)
     cp = _vector(codes, "codes", torch.int8, (m, n))
     zp = None if zeros is None else _vector(zeros, "zeros", torch.float32, (m,))
     Q, ldq = _out(out, (m, n), _FP8, codes.device, "out")
-    _check(lib.bakron_fp8_from_codes(cp, zp, m, n, kind, bits, Q.data_ptr(), ldq, _where(stream, Q)),
+    _check(lib.bakron_fp8_from_codes(cp, zp, m, n, kind, bits, Q.data_ptr(), ldq, _here()),
            "bakron_fp8_from_codes")
     return Q
 
@@ -414,6 +430,8 @@ def fp8_matmul(X, sx, W, sw, offsets=None, out_dtype=torch.bfloat16, out=None, d
     offsets (int32, groups + 1, on the GPU).  sw has one scale for each row of W,
     of shape (N,) or (groups, N), or one for each block, of shape (ceil(K / 128),
     ceil(N / 128)) or (groups, ...).  out_dtype: bfloat16 or float16."""
+    if _elsewhere(stream):
+        return _on(stream, fp8_matmul, X, sx, W, sw, offsets, out_dtype, out, dev_status)
     lib = load()
     ldx = _rows_of(X, "X", (_FP8,))
     ldw = _rows_of(W, "W", (_FP8,), 3 if W.dim() == 3 else 2)
@@ -435,11 +453,11 @@ def fp8_matmul(X, sx, W, sw, offsets=None, out_dtype=torch.bfloat16, out=None, d
     _check(lib.bakron_fp8_matmul(X.data_ptr(), ldx, sxp, W.data_ptr(), ldw, swp, wscale, rows, N, K, groups,
                                  op, Y.data_ptr(), _TYPES[out_dtype], ldy, _status(dev_status),
                                  None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                                 _where(stream, Y, ws)), "bakron_fp8_matmul")
+                                 _here()), "bakron_fp8_matmul")
     return Y
 
 
-def _grouped(fn, what, A, B, rows, N, K, groups, op, shape, out_dtype, out, dev_status, stream):
+def _grouped(fn, what, A, B, rows, N, K, groups, op, shape, out_dtype, out, dev_status):
     lib = load()
     lda = _rows_of(A, "the left operand", (torch.bfloat16, torch.float16))
     ldb = _rows_of(B, "the right operand", (A.dtype,), B.dim())
@@ -450,7 +468,7 @@ def _grouped(fn, what, A, B, rows, N, K, groups, op, shape, out_dtype, out, dev_
     ws = _space(lib.bakron_grouped_matmul_workspace_size(rows, N, K, groups), A.device)
     _check(fn(A.data_ptr(), _TYPES[A.dtype], lda, B.data_ptr(), ldb, rows, N, K, groups, op, Y.data_ptr(),
               _TYPES[dtype], ldy, _status(dev_status), None if ws is None else ws.data_ptr(),
-              0 if ws is None else ws.numel(), _where(stream, Y, ws)), what)
+              0 if ws is None else ws.numel(), _here()), what)
     return Y
 
 
@@ -458,18 +476,22 @@ def grouped_matmul(X, W, offsets=None, out_dtype=None, out=None, dev_status=None
     """Y[r] = X[r] W_g(r)^T (bakron_grouped_matmul).  X (rows, K) and W (groups, N, K)
     in bfloat16 or float16, offsets (int32, groups + 1, on the GPU): group g has the
     rows offsets[g] .. offsets[g + 1] - 1.  out_dtype: X's (the default) or float32."""
+    if _elsewhere(stream):
+        return _on(stream, grouped_matmul, X, W, offsets, out_dtype, out, dev_status)
     groups, op = _groups(W, offsets)
     if X.dim() != 2 or W.dim() not in (2, 3) or W.shape[-1] != X.shape[1]:
         raise BakronError(f"X {tuple(X.shape)} and W {tuple(W.shape)} do not fit")
     rows, K, N = X.shape[0], X.shape[1], W.shape[-2]
     return _grouped(load().bakron_grouped_matmul, "bakron_grouped_matmul", X, W, rows, N, K, groups, op,
-                    (rows, N), out_dtype, out, dev_status, stream)
+                    (rows, N), out_dtype, out, dev_status)
 
 
 def grouped_matmul_grad(dY, X, W, offsets=None, want_x=True, want_w=True, w_dtype=None, dev_status=None,
                         stream=None):
     """grouped_matmul's gradients (dX, dW) for dY (bakron_grouped_matmul_grad_x and
     _grad_w).  One that is not wanted is None.  w_dtype: X's (the default) or float32."""
+    if _elsewhere(stream):
+        return _on(stream, grouped_matmul_grad, dY, X, W, offsets, want_x, want_w, w_dtype, dev_status)
     groups, op = _groups(W, offsets)
     if X.dim() != 2 or W.dim() not in (2, 3) or W.shape[-1] != X.shape[1] or \
             tuple(dY.shape) != (X.shape[0], W.shape[-2]):
@@ -478,10 +500,10 @@ def grouped_matmul_grad(dY, X, W, offsets=None, want_x=True, want_w=True, w_dtyp
     lib, dX, dW = load(), None, None
     if want_x:
         dX = _grouped(lib.bakron_grouped_matmul_grad_x, "bakron_grouped_matmul_grad_x", dY, W, rows, N, K,
-                      groups, op, (rows, K), None, None, dev_status, stream)
+                      groups, op, (rows, K), None, None, dev_status)
     if want_w:
         dW = _grouped(lib.bakron_grouped_matmul_grad_w, "bakron_grouped_matmul_grad_w", dY, X, rows, N, K,
-                      groups, op, tuple(W.shape), w_dtype, None, dev_status, stream)
+                      groups, op, tuple(W.shape), w_dtype, None, dev_status)
     return dX, dW
 
 
@@ -489,6 +511,8 @@ def token_logprobs(logits, targets, top=0, dev_status=None, stream=None):
     """Log probabilities of the targets (int64, negative: none), with entropy and the
     `top` likeliest tokens (bakron_token_logprobs).  Returns a dict with logprob,
     lse, entropy (rows) and top_logprob, top_ids (rows, top; None for top 0)."""
+    if _elsewhere(stream):
+        return _on(stream, token_logprobs, logits, targets, top, dev_status)
     lib = load()
     ld = _rows_of(logits, "logits", _TYPES)
     rows, vocab = logits.shape
@@ -506,7 +530,7 @@ def token_logprobs(logits, targets, top=0, dev_status=None, stream=None):
                                      sp + 4 * rows, sp + 8 * rows, tl.data_ptr() if top else None,
                                      ti.data_ptr() if top else None, _status(dev_status),
                                      None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                                     _where(stream, stats, tl, ti, ws)), "bakron_token_logprobs")
+                                     _here()), "bakron_token_logprobs")
     return dict(logprob=logprob, lse=lse, entropy=entropy, top_logprob=tl, top_ids=ti)
 
 
@@ -514,6 +538,8 @@ def token_logprobs_grad(logits, targets, lse, entropy, g_logprob, g_entropy=None
                         stream=None):
     """The gradient of sum(g_logprob logprob + g_entropy entropy) with respect to the
     logits (bakron_token_logprobs_grad), from the forward call's lse and entropy."""
+    if _elsewhere(stream):
+        return _on(stream, token_logprobs_grad, logits, targets, lse, entropy, g_logprob, g_entropy, out, dev_status)
     lib = load()
     ld = _rows_of(logits, "logits", _TYPES)
     rows, vocab = logits.shape
@@ -526,5 +552,5 @@ def token_logprobs_grad(logits, targets, lse, entropy, g_logprob, g_entropy=None
         _vector(lse, "lse", f32, (rows,)), None if entropy is None else _vector(entropy, "entropy", f32, (rows,)),
         _vector(g_logprob, "g_logprob", f32, (rows,)),
         None if g_entropy is None else _vector(g_entropy, "g_entropy", f32, (rows,)), D.data_ptr(), ldd,
-        _status(dev_status), _where(stream, D)), "bakron_token_logprobs_grad")
+        _status(dev_status), _here()), "bakron_token_logprobs_grad")
     return D
