@@ -304,7 +304,8 @@ int32_t bakron_fp8_quantize(const void *X, int32_t type, int64_t rows, int64_t c
  * an integer in [-15, 15] for every kind and width accepted here (BAKRON_Q_SYM
  * and BAKRON_Q_ASYM with 2 to 4 bits).  With the solve's row scales,
  * bakron_fp8_matmul (BAKRON_SCALE_ROW) multiplies with V itself.
- *   codes  m x n (contiguous, as bakron_quantize writes them)
+ *   codes  m x n (contiguous, as bakron_quantize writes them); m, n <= 2^22,
+ *          m n <= 2^40
  *   zeros  m zero points for BAKRON_Q_ASYM, else NULL
  *   Q      m x n, row stride ldq
  */

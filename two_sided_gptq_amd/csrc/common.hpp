@@ -19,6 +19,10 @@ void clear_error();
 // device and cached), else BAKRON_ERR_UNSUPPORTED_DEVICE / BAKRON_ERR_HIP.
 int32_t check_device();
 
+// A launch has to stay below 2^32 threads in a dimension; beyond, some forms fail and
+// others run with what is left of the number in 32 bits.
+constexpr int64_t LAUNCH_THREADS = (int64_t(1) << 32) - 1;
+
 inline int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 

@@ -225,9 +225,13 @@ extern "C" int32_t bakron_fp8_from_codes(const int8_t *codes, const float *zeros
                "zeros go with asymmetric codes, and only with them");
     int32_t st = check_device();
     if (st != BAKRON_OK) return st;
-    const int64_t threads = m * ((n + 15) / 16);
-    hipLaunchKernelGGL(from_codes_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0,
-                       static_cast<hipStream_t>(stream_), codes, zeros, m, n, Q, ldq);
-    BK_LAUNCH_CHECK("from_codes_kernel");
+    const int64_t per_row = (n + 15) / 16, most = (LAUNCH_THREADS - 255) / per_row;  // rows of a launch
+    for (int64_t r = 0; r < m; r += most) {
+        const int64_t rows = m - r < most ? m - r : most;
+        hipLaunchKernelGGL(from_codes_kernel, dim3((unsigned)((rows * per_row + 255) / 256)), dim3(256), 0,
+                           static_cast<hipStream_t>(stream_), codes + r * n, zeros ? zeros + r : nullptr, rows, n,
+                           Q + r * ldq, ldq);
+        BK_LAUNCH_CHECK("from_codes_kernel");
+    }
     return BAKRON_OK;
 }
