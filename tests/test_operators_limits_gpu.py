@@ -16,6 +16,46 @@ def bk():
     torch.cuda.empty_cache()
 
 
+def rows_of(rows, vocab, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(rows, vocab, device="cuda", generator=g).bfloat16()
+    t = torch.randint(0, vocab, (rows,), device="cuda", generator=g)
+    t[::1001] = -1
+    return x, t
+
+
+def scores64(x, t):
+    x = x.double()
+    lse = x.logsumexp(1)
+    lp = x - lse[:, None]
+    return lse, -(lp.exp() * lp).sum(1), torch.where(t < 0, 0.0, lp.gather(1, t.clamp(min=0)[:, None])[:, 0]), lp
+
+
+# Values are off by at most 2^-20 (1 + |lse| + max |x|), gradients by 2^-20 (1 + |x| + |lse|)
+# of each term and one rounding to bf16.
+@pytest.mark.parametrize("rows", [(1 << 23) - 1, (1 << 23) + 5, 1 << 24])
+def test_token_logprobs_of_many_rows(bk, rows):
+    vocab, k = 3, 2
+    x, t = rows_of(rows, vocab, rows)
+    r = bk.token_logprobs(x, t, top=k)
+    g = torch.ones(rows, device="cuda")
+    d = bk.token_logprobs_grad(x, t, r["lse"], r["entropy"], g, g)
+    for a in range(0, rows, 1 << 21):
+        at = slice(a, min(rows, a + (1 << 21)))
+        lse, ent, logprob, lp = scores64(x[at], t[at])
+        tol = 2.0 ** -20 * (1 + lse.abs() + x[at].double().abs().amax(1))
+        for name, want in (("lse", lse), ("entropy", ent), ("logprob", logprob)):
+            assert bool(((r[name][at].double() - want).abs() <= tol).all()), (name, a)
+        v, i = torch.sort(x[at].double(), dim=1, descending=True, stable=True)
+        assert torch.equal(r["top_ids"][at], i[:, :k]), a
+        assert bool(((r["top_logprob"][at].double() - (v[:, :k] - lse[:, None])).abs() <= tol[:, None]).all()), a
+        p = lp.exp()
+        hit = torch.zeros_like(p).scatter_(1, t[at].clamp(min=0)[:, None], 1.0) * (t[at] >= 0)[:, None]
+        want = hit - p * (t[at] >= 0)[:, None] - p * (lp + ent[:, None])
+        slack = tol[:, None] * p * (3 + lp.abs() + ent[:, None]) + 2.0 ** -8 * want.abs() + 2.0 ** -24
+        assert bool(((d[at].double() - want).abs() <= slack).all()), a
+
+
 def test_codes_beyond_one_launch(bk):
     """2^36 codes and a row more: 64 GiB in, 64 GiB out."""
     m, n = (1 << 18) + 1, 1 << 18

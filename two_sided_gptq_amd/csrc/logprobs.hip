@@ -413,13 +413,43 @@ void layout(RowArgs &a) {
 }
 
 template <int T>
-void launch_rows(const RowArgs &a, hipStream_t s) {
+void launch_rows(const RowArgs &all, hipStream_t s) {
+    RowArgs a = all;
     if (a.segs == 1) {
-        hipLaunchKernelGGL(row_kernel<T>, dim3((unsigned)a.rows), dim3(NT), 0, s, a);
+        constexpr int64_t most = LAUNCH_THREADS / NT;
+        for (int64_t left = a.rows; left > 0; left -= most) {
+            a.rows = left < most ? left : most;
+            hipLaunchKernelGGL(row_kernel<T>, dim3((unsigned)a.rows), dim3(NT), 0, s, a);
+            a.x += a.rows * a.ld * elem_size(T), a.targets += a.rows;
+            a.logprob += a.rows, a.lse += a.rows, a.entropy += a.rows;
+            if (a.k) a.top_logprob += a.rows * a.k, a.top_ids += a.rows * a.k;
+        }
         return;
     }
     hipLaunchKernelGGL(part_kernel<T>, dim3((unsigned)(a.rows * a.segs)), dim3(NTS), 0, s, a);
     hipLaunchKernelGGL(join_kernel<T>, dim3((unsigned)a.rows), dim3(NT), 0, s, a);
+}
+
+struct GradArgs {
+    const char *x;
+    int64_t rows, vocab, ld;
+    const int64_t *targets;
+    const float *lse, *entropy, *g_logprob, *g_entropy;
+    char *dx;
+    int64_t ldd;
+    int32_t *dev_status;
+};
+
+template <int T>
+void launch_grad(const GradArgs &a, hipStream_t s) {
+    const int64_t segs = (a.vocab + 8191) / 8192, most = LAUNCH_THREADS / 256 / segs;  // rows of a launch
+    for (int64_t r = 0; r < a.rows; r += most) {
+        const int64_t rows = a.rows - r < most ? a.rows - r : most;
+        hipLaunchKernelGGL(grad_kernel<T>, dim3((unsigned)(rows * segs)), dim3(256), 0, s,
+                           a.x + r * a.ld * elem_size(T), a.vocab, a.ld, a.targets + r, a.lse + r,
+                           a.entropy ? a.entropy + r : nullptr, a.g_logprob + r, a.g_entropy ? a.g_entropy + r : nullptr,
+                           a.dx + r * a.ldd * elem_size(T), a.ldd, (int)segs, a.dev_status);
+    }
 }
 
 constexpr int64_t MAX_VOCAB = (int64_t)CHUNKS * CE * (CAP / KMAX);  // 2^21
@@ -503,24 +533,17 @@ extern "C" int32_t bakron_token_logprobs_grad(const void *logits, int32_t type, 
     BK_REQUIRE(((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dlogits)) &
                 (elem_size(type) - 1)) == 0,
                "logits or dlogits are misaligned for their type");
-    const int64_t segs = (vocab + 8191) / 8192;
-    BK_REQUIRE(rows * segs < (int64_t(1) << 31), "too many logits: rows=%lld vocab=%lld", (long long)rows,
-               (long long)vocab);
     int32_t st = check_device();
     if (st != BAKRON_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream_);
-    const dim3 grid((unsigned)(rows * segs));
-    const char *x = static_cast<const char *>(logits);
-    char *dx = static_cast<char *>(dlogits);
+    const GradArgs a = {static_cast<const char *>(logits), rows, vocab, ld, targets, lse, entropy, g_logprob, g_entropy,
+                        static_cast<char *>(dlogits), ldd, dev_status};
     if (type == BAKRON_T_F32)
-        hipLaunchKernelGGL(grad_kernel<BAKRON_T_F32>, grid, dim3(256), 0, s, x, vocab, ld, targets, lse,
-                           entropy, g_logprob, g_entropy, dx, ldd, (int)segs, dev_status);
+        launch_grad<BAKRON_T_F32>(a, s);
     else if (type == BAKRON_T_BF16)
-        hipLaunchKernelGGL(grad_kernel<BAKRON_T_BF16>, grid, dim3(256), 0, s, x, vocab, ld, targets, lse,
-                           entropy, g_logprob, g_entropy, dx, ldd, (int)segs, dev_status);
+        launch_grad<BAKRON_T_BF16>(a, s);
     else
-        hipLaunchKernelGGL(grad_kernel<BAKRON_T_F16>, grid, dim3(256), 0, s, x, vocab, ld, targets, lse,
-                           entropy, g_logprob, g_entropy, dx, ldd, (int)segs, dev_status);
+        launch_grad<BAKRON_T_F16>(a, s);
     BK_LAUNCH_CHECK("grad_kernel");
     return BAKRON_OK;
 }
