@@ -273,7 +273,8 @@ int32_t bakron_last_phase_ms(double *out);
  * expert where a layer has experts, and what says how a model's answers moved.
  * For these calls a matrix's rows may be `ld` elements apart (ld >= its width;
  * any ld and any alignment of one element are accepted, rows that begin on 16
- * bytes are faster).  Sizes are 1 to 2^24 unless noted; groups may be empty.
+ * bytes are faster).  Sizes are 1 to 2^24 unless noted, groups 1 to 4096; groups
+ * may be empty.  A product whose tiles need 2^32 threads or more is refused.
  */
 
 /* element types */

@@ -1086,16 +1086,36 @@ size_t parts_size(int mode, int es, int64_t rows, int64_t I, int64_t J, int64_t 
     return (size_t)(tiles * s) * 128 * 128 * sizeof(float);
 }
 
-// About 4096 waves, 16 a CU, keep enough loads under way: as many parts of the
-// reduction as that takes, or sets of rows of W where one part does.
+// The parts of the reduction, wk, and the sets of rows of W, wn, of product_few_kernel's
+// workgroups.  About 4096 waves, 16 a CU, keep enough loads under way: as many parts of
+// the reduction as that takes, or sets of rows of W where one part does.
+void few_waves(int es, int64_t rows, int64_t J, int64_t R, int groups, bool grouped, int &wn, int &wk) {
+    const int64_t blocks = (R * es + STEP - 1) / STEP;
+    const int64_t slots = grouped ? std::min<int64_t>(groups, rows) : (rows + 15) / 16;
+    const int64_t sets = slots * ((J + 15) / 16);
+    wk = 1;
+    while (wk < 16 && wk * 2 * sets <= 4096 && wk * 2 <= blocks) wk *= 2;
+    wn = wk >= 4 ? 1 : 4 / wk;
+}
+
+// Threads of the largest launch of a product, whichever form its operands' alignment
+// calls for; rows after the last group's count too.  Split reductions are of few tiles.
+int64_t launch_threads(int mode, int es, int64_t rows, int64_t I, int64_t J, int64_t R, int groups, bool grouped) {
+    if (mode == FWD && few_rows(rows, groups, grouped)) {
+        int wn, wk;
+        few_waves(es, rows, J, R, groups, grouped, wn, wk);
+        return row_tiles(16, rows, groups, grouped) * ((J + 16 * wn - 1) / (16 * wn)) * 64 * wn * wk;
+    }
+    auto tiles = [&](int64_t b) {
+        return (mode == GRAD_W ? groups * ((I + b - 1) / b) : row_tiles(b, rows, groups, grouped)) * ((J + b - 1) / b);
+    };
+    return std::max(tiles(128) * 256, (tiles(256) + 7 + TAIL_MOST) * 512);
+}
+
 template <int ET, int SCALE>
 void launch_few(ProductArgs &p, hipStream_t s) {
-    const int64_t blocks = (p.R * (ET == F8 ? 1 : 2) + STEP - 1) / STEP;
-    const int64_t slots = p.offsets ? std::min<int64_t>(p.groups, p.rows) : (p.rows + 15) / 16;
-    const int64_t sets = slots * ((p.J + 15) / 16);
-    int wk = 1;
-    while (wk < 16 && wk * 2 * sets <= 4096 && wk * 2 <= blocks) wk *= 2;
-    const int wn = wk >= 4 ? 1 : 4 / wk;
+    int wn, wk;
+    few_waves(ET == F8 ? 1 : 2, p.rows, p.J, p.R, p.groups, p.offsets != nullptr, wn, wk);
     p.tiles_j = (int)((p.J + 16 * wn - 1) / (16 * wn));
     p.slots = (int)row_tiles(16, p.rows, p.groups, p.offsets != nullptr);
     const int64_t grid = (int64_t)p.slots * p.tiles_j;
@@ -1162,15 +1182,17 @@ bool sizes_ok(int64_t rows, int64_t N, int64_t K, int32_t groups) {
 }
 
 // Limits that keep every index in range: no size over 2^24, no more than 2^31
-// workgroups of the smallest tiles.
-int32_t check_sizes(int64_t rows, int64_t N, int64_t K, int32_t groups, const int32_t *offsets) {
+// workgroups of the smallest tiles, no launch of more threads than there can be.
+int32_t check_sizes(int mode, int es, int64_t rows, int64_t N, int64_t K, int32_t groups, const int32_t *offsets) {
     BK_REQUIRE(rows >= 1 && N >= 1 && K >= 1 && rows <= MAX_DIM && N <= MAX_DIM && K <= MAX_DIM,
                "bad sizes rows=%lld N=%lld K=%lld", (long long)rows, (long long)N, (long long)K);
     BK_REQUIRE(groups >= 1 && groups <= MAX_GROUPS, "groups must be in 1 .. %d, not %d", MAX_GROUPS, groups);
     BK_REQUIRE(offsets || groups == 1, "offsets must be non-NULL for %d groups", groups);
+    const int64_t I = mode == GRAD_W ? N : rows, J = mode == FWD ? N : K, R = mode == FWD ? K : mode == GRAD_X ? N : 0;
     BK_REQUIRE((rows / 16 + 1 + groups + 1) * (N / 16 + 1) < (int64_t(1) << 31) &&
                    (rows / 16 + 1 + groups + 1) * (K / 16 + 1) < (int64_t(1) << 31) &&
-                   (int64_t)groups * (N / 64 + 1) * (K / 64 + 1) < (int64_t(1) << 31),
+                   (int64_t)groups * (N / 64 + 1) * (K / 64 + 1) < (int64_t(1) << 31) &&
+                   launch_threads(mode, es, rows, I, J, R, groups, offsets != nullptr) <= LAUNCH_THREADS,
                "too many tiles: rows=%lld N=%lld K=%lld groups=%d", (long long)rows, (long long)N,
                (long long)K, groups);
     return BAKRON_OK;
@@ -1249,7 +1271,7 @@ extern "C" int32_t bakron_fp8_matmul(const uint8_t *X, int64_t ldx, const float 
     clear_error();
     BK_REQUIRE(X && sx && W && sw && Y, "X, sx, W, sw and Y must be non-NULL");
     BK_REQUIRE(wscale == BAKRON_SCALE_ROW || wscale == BAKRON_SCALE_BLOCK, "bad weight scale kind %d", wscale);
-    BK_TRY(check_sizes(rows, N, K, groups, offsets));
+    BK_TRY(check_sizes(FWD, 1, rows, N, K, groups, offsets));
     BK_TRY(check_ld("ldx", ldx, K, rows));
     BK_TRY(check_ld("ldw", ldw, K, groups * N));
     BK_TRY(check_ld("ldy", ldy, N, rows));
@@ -1281,7 +1303,7 @@ extern "C" int32_t bakron_grouped_matmul(const void *X, int32_t type, int64_t ld
     clear_error();
     BK_REQUIRE(X && W && Y, "X, W and Y must be non-NULL");
     BK_TRY(check_type16(type));
-    BK_TRY(check_sizes(rows, N, K, groups, offsets));
+    BK_TRY(check_sizes(FWD, 2, rows, N, K, groups, offsets));
     BK_TRY(check_ld("ldx", ldx, K, rows));
     BK_TRY(check_ld("ldw", ldw, K, groups * N));
     BK_TRY(check_ld("ldy", ldy, N, rows));
@@ -1312,7 +1334,7 @@ extern "C" int32_t bakron_grouped_matmul_grad_x(const void *dY, int32_t type, in
     clear_error();
     BK_REQUIRE(dY && W && dX, "dY, W and dX must be non-NULL");
     BK_TRY(check_type16(type));
-    BK_TRY(check_sizes(rows, N, K, groups, offsets));
+    BK_TRY(check_sizes(GRAD_X, 2, rows, N, K, groups, offsets));
     BK_TRY(check_ld("lddy", lddy, N, rows));
     BK_TRY(check_ld("ldw", ldw, K, groups * N));
     BK_TRY(check_ld("lddx", lddx, K, rows));
@@ -1343,7 +1365,7 @@ extern "C" int32_t bakron_grouped_matmul_grad_w(const void *dY, int32_t type, in
     clear_error();
     BK_REQUIRE(dY && X && dW, "dY, X and dW must be non-NULL");
     BK_TRY(check_type16(type));
-    BK_TRY(check_sizes(rows, N, K, groups, offsets));
+    BK_TRY(check_sizes(GRAD_W, 2, rows, N, K, groups, offsets));
     BK_TRY(check_ld("lddy", lddy, N, rows));
     BK_TRY(check_ld("ldx", ldx, K, rows));
     BK_TRY(check_ld("lddw", lddw, K, groups * N));
