@@ -332,9 +332,10 @@ def _rows_of(t, name, dtypes, ndim=2):
 
 
 def _vector(t, name, dtype, shape):
-    """t's pointer if it is a contiguous GPU tensor of this dtype and shape."""
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise BakronError(f"{name} must be a contiguous {dtype} GPU tensor of shape {tuple(shape)}")
+    """t's pointer if it is a contiguous tensor of this dtype and shape on the current GPU."""
+    dev = t.get_device()
+    if t.dtype != dtype or t.shape != shape or dev < 0 or dev != torch._C._cuda_getDevice() or not t.is_contiguous():
+        raise BakronError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the current GPU")
     return t.data_ptr()
 
 
