@@ -18,7 +18,7 @@ def test_vectors_of_another_gpu_are_refused(bk, monkeypatch):
     """Offsets, scales, targets and the like: with another GPU current, as matrices are."""
     v = torch.zeros(4, device="cuda")
     assert bk._vector(v, "v", torch.float32, (4,)) == v.data_ptr()
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    monkeypatch.setattr(bk, "_device", lambda: 1)
     with pytest.raises(bk.BakronError, match="current GPU"):
         bk._vector(v, "v", torch.float32, (4,))
     monkeypatch.undo()

@@ -311,12 +311,14 @@ def last_phase_ms() -> dict:
 
 _TYPES = {torch.float32: T_F32, torch.bfloat16: T_BF16, torch.float16: T_F16}
 _FP8 = torch.float8_e4m3fn
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _rows_of(t, name, dtypes, ndim=2):
     """The element distance between t's rows, after the checks that every matrix gets."""
     shape, stride, dev = t.shape, t.stride(), t.get_device()
-    if dev < 0 or dev != torch._C._cuda_getDevice():
+    if dev < 0 or dev != _device():
         raise BakronError(f"{name} must be on the current GPU")
     if t.dtype not in dtypes:
         raise BakronError(f"{name} must be one of {[str(d) for d in dtypes]}, not {t.dtype}")
@@ -334,7 +336,7 @@ def _rows_of(t, name, dtypes, ndim=2):
 def _vector(t, name, dtype, shape):
     """t's pointer if it is a contiguous tensor of this dtype and shape on the current GPU."""
     dev = t.get_device()
-    if t.dtype != dtype or t.shape != shape or dev < 0 or dev != torch._C._cuda_getDevice() or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or dev < 0 or dev != _device() or not t.is_contiguous():
         raise BakronError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the current GPU")
     return t.data_ptr()
 
@@ -350,7 +352,7 @@ def _out(out, shape, dtype, device, name):
 
 def _here():
     """The handle of torch's current stream."""
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _raw_stream(_device())
 
 
 def _elsewhere(stream):
