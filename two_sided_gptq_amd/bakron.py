@@ -307,7 +307,8 @@ def last_phase_ms() -> dict:
 # Operators for rounded layers.  Matrices are GPU tensors whose rows may lie apart
 # (a row's elements are adjacent); nothing is copied to make them contiguous.
 # `stream`: where the call runs, by default torch's current stream; inputs and given
-# outputs have to be ready for it.
+# outputs have to be ready for it.  Inputs of 0 rows (no tokens) give outputs of 0 rows,
+# and gradients of weights that are 0, without a call of the library.
 
 _TYPES = {torch.float32: T_F32, torch.bfloat16: T_BF16, torch.float16: T_F16}
 _FP8 = torch.float8_e4m3fn
@@ -315,14 +316,15 @@ _device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _rows_of(t, name, dtypes, ndim=2):
-    """The element distance between t's rows, after the checks that every matrix gets."""
+def _rows_of(t, name, dtypes, ndim=2, empty=False):
+    """The element distance between t's rows, after the checks that every matrix gets.
+    empty: there may be no rows."""
     shape, stride, dev = t.shape, t.stride(), t.get_device()
     if dev < 0 or dev != _device():
         raise BakronError(f"{name} must be on the current GPU")
     if t.dtype not in dtypes:
         raise BakronError(f"{name} must be one of {[str(d) for d in dtypes]}, not {t.dtype}")
-    if len(shape) != ndim or 0 in shape:
+    if len(shape) != ndim or 0 in shape and not (empty and shape[-1] and not shape[-2]):
         raise BakronError(f"{name} must have {ndim} dimensions, none of size 0, not {tuple(shape)}")
     n, k = shape[-2], shape[-1]
     if k != 1 and stride[-1] != 1:
@@ -347,7 +349,7 @@ def _out(out, shape, dtype, device, name):
         return torch.empty(shape, dtype=dtype, device=device), shape[-1]
     if out.shape != shape or out.dtype != dtype:
         raise BakronError(f"{name} must be {dtype} of shape {tuple(shape)}")
-    return out, _rows_of(out, name, (dtype,), len(shape))
+    return out, _rows_of(out, name, (dtype,), len(shape), 0 in shape)
 
 
 def _here():
@@ -383,7 +385,7 @@ def fp8_quantize(X, block_rows=1, out=None, scales=None, dev_status=None, stream
     if _elsewhere(stream):
         return _on(stream, fp8_quantize, X, block_rows, out, scales, dev_status)
     lib = load()
-    ldx = _rows_of(X, "X", _TYPES)
+    ldx = _rows_of(X, "X", _TYPES, empty=True)
     rows, cols = X.shape
     if block_rows not in (1, 128):
         raise BakronError(f"block_rows must be 1 or 128, not {block_rows}")
@@ -391,6 +393,8 @@ def fp8_quantize(X, block_rows=1, out=None, scales=None, dev_status=None, stream
     of = (-(-cols // 128), -(-rows // block_rows))
     S = torch.empty(of, dtype=torch.float32, device=X.device) if scales is None else scales
     sp = S.data_ptr() if scales is None else _vector(S, "scales", torch.float32, of)
+    if rows == 0:
+        return Q, S
     _check(lib.bakron_fp8_quantize(X.data_ptr(), _TYPES[X.dtype], rows, cols, ldx, block_rows, Q.data_ptr(),
                                    ldq, sp, _status(dev_status), _here()), "bakron_fp8_quantize")
     return Q, S
@@ -436,7 +440,7 @@ def fp8_matmul(X, sx, W, sw, offsets=None, out_dtype=torch.bfloat16, out=None, d
     if _elsewhere(stream):
         return _on(stream, fp8_matmul, X, sx, W, sw, offsets, out_dtype, out, dev_status)
     lib = load()
-    ldx = _rows_of(X, "X", (_FP8,))
+    ldx = _rows_of(X, "X", (_FP8,), empty=True)
     ldw = _rows_of(W, "W", (_FP8,), 3 if W.dim() == 3 else 2)
     rows, K = X.shape
     N = W.shape[-2]
@@ -452,6 +456,8 @@ def fp8_matmul(X, sx, W, sw, offsets=None, out_dtype=torch.bfloat16, out=None, d
     if out_dtype not in (torch.bfloat16, torch.float16):
         raise BakronError(f"out_dtype must be bfloat16 or float16, not {out_dtype}")
     Y, ldy = _out(out, (rows, N), out_dtype, X.device, "out")
+    if rows == 0:
+        return Y
     ws = _space(lib.bakron_fp8_matmul_workspace_size(rows, N, K, groups), X.device)
     _check(lib.bakron_fp8_matmul(X.data_ptr(), ldx, sxp, W.data_ptr(), ldw, swp, wscale, rows, N, K, groups,
                                  op, Y.data_ptr(), _TYPES[out_dtype], ldy, _status(dev_status),
@@ -460,14 +466,17 @@ def fp8_matmul(X, sx, W, sw, offsets=None, out_dtype=torch.bfloat16, out=None, d
     return Y
 
 
-def _grouped(fn, what, A, B, rows, N, K, groups, op, shape, out_dtype, out, dev_status):
+def _grouped(fn, what, A, B, rows, N, K, groups, op, shape, out_dtype, out, dev_status, over_rows=False):
+    """over_rows: the sums run over the rows, which both operands have."""
     lib = load()
-    lda = _rows_of(A, "the left operand", (torch.bfloat16, torch.float16))
-    ldb = _rows_of(B, "the right operand", (A.dtype,), B.dim())
+    lda = _rows_of(A, "the left operand", (torch.bfloat16, torch.float16), empty=True)
+    ldb = _rows_of(B, "the right operand", (A.dtype,), B.dim(), over_rows)
     dtype = A.dtype if out_dtype is None else out_dtype
     if dtype not in (A.dtype, torch.float32):
         raise BakronError(f"the output's dtype must be {A.dtype} or float32, not {dtype}")
     Y, ldy = _out(out, shape, dtype, A.device, "out")
+    if rows == 0:
+        return Y.zero_()  # sums over no rows, or no elements
     ws = _space(lib.bakron_grouped_matmul_workspace_size(rows, N, K, groups), A.device)
     _check(fn(A.data_ptr(), _TYPES[A.dtype], lda, B.data_ptr(), ldb, rows, N, K, groups, op, Y.data_ptr(),
               _TYPES[dtype], ldy, _status(dev_status), None if ws is None else ws.data_ptr(),
@@ -506,7 +515,7 @@ def grouped_matmul_grad(dY, X, W, offsets=None, want_x=True, want_w=True, w_dtyp
                       groups, op, (rows, K), None, None, dev_status)
     if want_w:
         dW = _grouped(lib.bakron_grouped_matmul_grad_w, "bakron_grouped_matmul_grad_w", dY, X, rows, N, K,
-                      groups, op, tuple(W.shape), w_dtype, None, dev_status)
+                      groups, op, tuple(W.shape), w_dtype, None, dev_status, over_rows=True)
     return dX, dW
 
 
@@ -517,7 +526,7 @@ def token_logprobs(logits, targets, top=0, dev_status=None, stream=None):
     if _elsewhere(stream):
         return _on(stream, token_logprobs, logits, targets, top, dev_status)
     lib = load()
-    ld = _rows_of(logits, "logits", _TYPES)
+    ld = _rows_of(logits, "logits", _TYPES, empty=True)
     rows, vocab = logits.shape
     tp = _vector(targets, "targets", torch.int64, (rows,))
     if not 0 <= top <= min(64, vocab):
@@ -527,13 +536,14 @@ def token_logprobs(logits, targets, top=0, dev_status=None, stream=None):
     logprob, lse, entropy = stats.unbind()
     tl = torch.empty((rows, top), dtype=torch.float32, device=dev) if top else None
     ti = torch.empty((rows, top), dtype=torch.int64, device=dev) if top else None
-    ws = _space(lib.bakron_token_logprobs_workspace_size(rows, vocab, top), dev)
-    sp = stats.data_ptr()
-    _check(lib.bakron_token_logprobs(logits.data_ptr(), _TYPES[logits.dtype], rows, vocab, ld, tp, top, sp,
-                                     sp + 4 * rows, sp + 8 * rows, tl.data_ptr() if top else None,
-                                     ti.data_ptr() if top else None, _status(dev_status),
-                                     None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                                     _here()), "bakron_token_logprobs")
+    if rows:
+        ws = _space(lib.bakron_token_logprobs_workspace_size(rows, vocab, top), dev)
+        sp = stats.data_ptr()
+        _check(lib.bakron_token_logprobs(logits.data_ptr(), _TYPES[logits.dtype], rows, vocab, ld, tp, top, sp,
+                                         sp + 4 * rows, sp + 8 * rows, tl.data_ptr() if top else None,
+                                         ti.data_ptr() if top else None, _status(dev_status),
+                                         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                                         _here()), "bakron_token_logprobs")
     return dict(logprob=logprob, lse=lse, entropy=entropy, top_logprob=tl, top_ids=ti)
 
 
@@ -544,16 +554,18 @@ def token_logprobs_grad(logits, targets, lse, entropy, g_logprob, g_entropy=None
     if _elsewhere(stream):
         return _on(stream, token_logprobs_grad, logits, targets, lse, entropy, g_logprob, g_entropy, out, dev_status)
     lib = load()
-    ld = _rows_of(logits, "logits", _TYPES)
+    ld = _rows_of(logits, "logits", _TYPES, empty=True)
     rows, vocab = logits.shape
     f32 = torch.float32
     D, ldd = _out(out, (rows, vocab), logits.dtype, logits.device, "out")
     if g_entropy is not None and entropy is None:
         raise BakronError("g_entropy needs the forward call's entropy")
-    _check(lib.bakron_token_logprobs_grad(
-        logits.data_ptr(), _TYPES[logits.dtype], rows, vocab, ld, _vector(targets, "targets", torch.int64, (rows,)),
-        _vector(lse, "lse", f32, (rows,)), None if entropy is None else _vector(entropy, "entropy", f32, (rows,)),
-        _vector(g_logprob, "g_logprob", f32, (rows,)),
-        None if g_entropy is None else _vector(g_entropy, "g_entropy", f32, (rows,)), D.data_ptr(), ldd,
-        _status(dev_status), _here()), "bakron_token_logprobs_grad")
+    vectors = (_vector(targets, "targets", torch.int64, (rows,)), _vector(lse, "lse", f32, (rows,)),
+               None if entropy is None else _vector(entropy, "entropy", f32, (rows,)),
+               _vector(g_logprob, "g_logprob", f32, (rows,)),
+               None if g_entropy is None else _vector(g_entropy, "g_entropy", f32, (rows,)))
+    if rows:
+        _check(lib.bakron_token_logprobs_grad(logits.data_ptr(), _TYPES[logits.dtype], rows, vocab, ld, *vectors,
+                                              D.data_ptr(), ldd, _status(dev_status), _here()),
+               "bakron_token_logprobs_grad")
     return D
