@@ -63,3 +63,20 @@ def test_no_rows(bk, groups):
                  lambda: bk.grouped_matmul(x, w, off, out=torch.empty(1, N, device="cuda", dtype=torch.bfloat16))):
         with pytest.raises(bk.BakronError):
             call()
+
+
+def test_groups_of_one_row(bk):
+    """Weights of one row a group: the stride inside a group means nothing, the groups' is
+    the distance between rows."""
+    g = torch.Generator().manual_seed(2)
+    full = torch.randn(5, 4, 64, generator=g).bfloat16().cuda()
+    x = torch.randn(40, 64, generator=g).bfloat16().cuda()
+    off = torch.tensor([0, 8, 16, 16, 30, 40], dtype=torch.int32, device="cuda")
+    for w in (full[:, :1], full[:, 2:3], full[:, 0].contiguous().unsqueeze(0).transpose(0, 1)):
+        assert w.shape == (5, 1, 64)
+        assert torch.equal(bk.grouped_matmul(x, w, off), bk.grouped_matmul(x, w.clone(memory_format=torch.contiguous_format), off))
+        dy = torch.ones(40, 1, device="cuda", dtype=torch.bfloat16)
+        a, b = bk.grouped_matmul_grad(dy, x, w, off), bk.grouped_matmul_grad(dy, x, w.clone(memory_format=torch.contiguous_format), off)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    with pytest.raises(bk.BakronError, match="rows apart"):
+        bk.grouped_matmul(x, full[:, :2], off)

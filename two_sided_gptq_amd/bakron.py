@@ -329,7 +329,10 @@ def _rows_of(t, name, dtypes, ndim=2, empty=False):
     n, k = shape[-2], shape[-1]
     if k != 1 and stride[-1] != 1:
         raise BakronError(f"the elements of a row of {name} must be adjacent")
-    ld = stride[-2] if n != 1 else max(stride[-2], k)
+    if n != 1:
+        ld = stride[-2]
+    else:  # one row, or one in each of several matrices
+        ld = stride[0] if ndim == 3 and shape[0] != 1 else max(stride[-2], k)
     if ndim == 3 and shape[0] != 1 and stride[0] != n * ld:
         raise BakronError(f"the matrices of {name} must lie {n} rows apart")
     return ld
