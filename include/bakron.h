@@ -369,6 +369,8 @@ int32_t bakron_grouped_matmul_grad_w(const void *dY, int32_t type, int64_t lddy,
  * bakron_token_logprobs -- log probabilities of given tokens, with entropy and
  * the k likeliest tokens.  Per row of logits x:
  *   lse = log sum_j e^x_j;  logprob = x_target - lse;  entropy = -sum_j p_j log p_j
+ *        (log probabilities are not taken from the rounded lse: with |lse| large,
+ *        as in a row of the type's lowest value, they hold more than it does)
  *   top: the k largest log probabilities and their tokens, in falling order,
  *        equal values by lowest index.
  *   logits   rows x vocab, `type` BAKRON_T_*, row stride ld.  -inf masks a token.
@@ -390,8 +392,13 @@ int32_t bakron_token_logprobs(const void *logits, int32_t type, int64_t rows, in
  * bakron_token_logprobs_grad -- the gradient of sum_r (g_logprob logprob +
  * g_entropy entropy) with respect to the logits:
  *   dlogits_j = g_logprob ([j = target] - p_j) - g_entropy p_j (log p_j + entropy)
- * from the forward call's lse and entropy.  Rows without a target have no first
- * term, rows of -inf only get 0.  g_entropy may be NULL (then entropy may be).
+ * from the forward call's lse and entropy.  p_j = e^(x_j - lse) of lse as given,
+ * an fp32 value: its rounding is p's relative error, 2^-15 at |lse| = 1024, and
+ * a row of fp32's or bf16's lowest value only, where lse holds nothing of log s,
+ * has p = 1 throughout; such rows should be masked with -inf.
+ * Rows without a target have no first term, rows of -inf only get 0.  A target
+ * >= vocab sets BAKRON_DEV_BAD_INDEX; its row then has the terms in p only.
+ * g_entropy may be NULL (then entropy may be).
  * dlogits has the logits' type, row stride ldd.  With g_logprob = 1 its rows are
  * the last layer's output-side samples (bakron_hessian).
  */

@@ -2,9 +2,10 @@
 //
 // For a row of logits x over a vocabulary of V tokens, with m = max x,
 // s = sum e^(x - m) and t = sum e^(x - m) (x - m):
-//   lse = m + log s,  log p_j = x_j - lse,  H = -sum p log p = log s - t / s.
-// One pass over the row keeps (m, s, t) and rescales the two sums where the
-// maximum grows; sums and statistics are fp32.
+//   lse = m + log s,  log p_j = (x_j - m) - log s,  H = -sum p log p = log s - t / s.
+// (x_j - lse would lose log s where |m| is large: in a row of the type's lowest value
+// every token would get the probability 1.)  One pass over the row keeps (m, s, t) and
+// rescales the two sums where the maximum grows; sums and statistics are fp32.
 //
 // Alternatives (the k largest, equal values by lowest index).  Each thread reads
 // chunks of consecutive elements and leaves each chunk's maximum.  An element of the k
@@ -138,14 +139,21 @@ __device__ __forceinline__ Target target_of(const RowArgs &a, int64_t row) {
     return r;
 }
 
+// What log probabilities are taken from: log p = (x - m) - logs.  logs is -inf in a row
+// without a distribution and NaN in one that holds a NaN or +inf.
+struct Norm {
+    float m, logs;
+    __device__ __forceinline__ float operator()(float x) const { return logs == -INFINITY ? -INFINITY : (x - m) - logs; }
+};
+
 // What a row's statistics give; one thread.
-__device__ __forceinline__ float finish_row(const RowArgs &a, int64_t row, Stats st, Target target) {
+__device__ __forceinline__ Norm finish_row(const RowArgs &a, int64_t row, Stats st, Target target) {
     const bool none = st.s == 0.0f;                    // every logit is -inf
     const bool bad = st.s != st.s || st.m > 3.4028235e38f;  // a NaN or +inf
     const float nan = __uint_as_float(0x7fc00000u);
-    const float logs = __logf(st.s);
-    float lse = none ? -INFINITY : st.m + logs;
-    float ent = none ? 0.0f : logs - st.t / st.s;
+    const Norm norm = {st.m, bad ? nan : none ? -INFINITY : __logf(st.s)};
+    float lse = none ? -INFINITY : st.m + norm.logs;
+    float ent = none ? 0.0f : norm.logs - st.t / st.s;
     if (bad) lse = ent = nan;
     int32_t flag = bad ? BAKRON_DEV_NONFINITE : 0;
     a.lse[row] = lse;
@@ -155,18 +163,17 @@ __device__ __forceinline__ float finish_row(const RowArgs &a, int64_t row, Stats
         lp = nan;
         flag |= BAKRON_DEV_BAD_INDEX;
     } else if (target.t >= 0) {
-        lp = none ? -INFINITY : target.x - lse;
+        lp = norm(target.x);
     }
     a.logprob[row] = lp;
     if (flag && a.dev_status) atomicOr(a.dev_status, flag);
-    return lse;
+    return norm;
 }
 
-__device__ __forceinline__ void write_top(const RowArgs &a, int64_t row, const uint64_t *best, float lse) {
+__device__ __forceinline__ void write_top(const RowArgs &a, int64_t row, const uint64_t *best, Norm norm) {
     for (int i = threadIdx.x; i < a.k; i += blockDim.x) {
         const uint64_t key = best[i];
-        const float x = unorder((uint32_t)(key >> 32));
-        a.top_logprob[row * a.k + i] = lse == -INFINITY ? -INFINITY : x - lse;
+        a.top_logprob[row * a.k + i] = norm(unorder((uint32_t)(key >> 32)));
         a.top_ids[row * a.k + i] = (int64_t)(uint32_t)~(uint32_t)key;
     }
 }
@@ -316,17 +323,17 @@ template <int T>
 __global__ __launch_bounds__(NT) void row_kernel(RowArgs a) {
     __shared__ TopSpace top;
     __shared__ Stats wave_part[NT / 64];
-    __shared__ float row_lse;
+    __shared__ Norm norm;
     const int64_t row = blockIdx.x, base = row * a.ld;
     Target target = {-1, 0.0f};
     if (threadIdx.x == 0) target = target_of<T>(a, row);
     Stats st = take_chunks<T, NT>(a, base, 0, a.chunks, a.k ? top.cmax : nullptr);
     st = block_stats<NT>(st, wave_part);
-    if (threadIdx.x == 0) row_lse = finish_row(a, row, st, target);
+    if (threadIdx.x == 0) norm = finish_row(a, row, st, target);
     if (a.k == 0) return;
     __syncthreads();
     select_top<T>(a, base, top);
-    write_top(a, row, top.best, row_lse);
+    write_top(a, row, top.best, norm);
 }
 
 // One part of a row.
@@ -345,7 +352,7 @@ __global__ __launch_bounds__(NTS) void part_kernel(RowArgs a) {
 template <int T>
 __global__ __launch_bounds__(NT) void join_kernel(RowArgs a) {
     __shared__ TopSpace top;
-    __shared__ float row_lse;
+    __shared__ Norm norm;
     const int64_t row = blockIdx.x;
     Target target = {-1, 0.0f};
     if (threadIdx.x == 0) target = target_of<T>(a, row);
@@ -356,15 +363,16 @@ __global__ __launch_bounds__(NT) void join_kernel(RowArgs a) {
         Stats st = {-3.4028235e38f, 0.0f, 0.0f};
         for (int i = threadIdx.x; i < a.segs; i += 64) st = merge(st, a.part[row * a.segs + i]);
         st = wave_stats(st);
-        if (threadIdx.x == 0) row_lse = finish_row(a, row, st, target);
+        if (threadIdx.x == 0) norm = finish_row(a, row, st, target);
     }
     if (a.k == 0) return;
     __syncthreads();
     select_top<T>(a, row * a.ld, top);
-    write_top(a, row, top.best, row_lse);
+    write_top(a, row, top.best, norm);
 }
 
-// d logits = -p (g + g_H (log p + H)), and g more at the target.
+// d logits = -p (g + g_H (log p + H)), and g more at the target.  log p = x - lse: of the
+// row's statistics the backward pass has no more.
 template <int T>
 __global__ __launch_bounds__(256) void grad_kernel(const char *__restrict__ x, int64_t vocab, int64_t ld,
                                                    const int64_t *__restrict__ targets,
