@@ -301,7 +301,8 @@ __device__ __forceinline__ floatx4 mfma(intx4 a, intx4 b, floatx4 c) {
 // The same in place, on accumulation registers.  Written out because the compiler
 // moves accumulators about when they fill all 256 of these registers.  It does not
 // see the hazards of this form: settle() stands between other accesses of the
-// accumulators and these products, in both directions.
+// accumulators and these products, in both directions.  That nothing else comes too
+// close is checked in the assembly of each build (tests/test_products_assembly.py).
 template <int ET>
 __device__ __forceinline__ void mfma_in_place(intx4 a, intx4 b, floatx4 &c) {
     if constexpr (ET == BAKRON_T_BF16)
@@ -583,7 +584,9 @@ __global__ __launch_bounds__(64 * WI * WJ) void product_kernel(ProductArgs p) {
 __device__ const uint4 zero_chunk = {0, 0, 0, 0};
 
 // Loads 16 bytes a lane straight into LDS, lane l's at `lds` + 16 l (wave uniform).
-// The wait for them is stage_wait's: the compiler does not count these loads.
+// The wait for them is stage_wait's: the compiler does not count these loads.  m0 is the
+// compiler's own and cannot be declared; it has no use for it in these kernels, which is
+// checked with the rest of the assembly, as is the distance from what computes `base`.
 __device__ __forceinline__ void load_lds(const char *base, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
                  : "memory");
