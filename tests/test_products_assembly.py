@@ -162,3 +162,18 @@ GOOD = dict(early="v_mov_b32_e32 v20, 0", wait=15, scalar="v_readfirstlane_b32 s
 def test_mistakes_are_found(change, count):
     (code,) = functions(CODE.format(**{**GOOD, **change})).values()
     assert len(hazards(code)) == count, hazards(code)
+
+
+@pytest.mark.parametrize("nj,fits", [(8, True), (16, False)])
+def test_rows_of_results_fit_the_swizzle(tmp_path, nj, fits):
+    """store_tile's rows of 2 NJ chunks are found again only if their 16 places repeat every 16 rows."""
+    if not os.path.exists(build.hipcc()):
+        pytest.skip("hipcc is missing")
+    use = tmp_path / "use.hip"
+    use.write_text(f'#include "{SOURCE}"\nnamespace bakron {{ namespace {{\n__global__ void use(ProductArgs p, char *s) {{\n'
+                   f'    floatx4 acc[2][{nj}] = {{}};\n    store_tile<SCALE_NONE, 2, {nj}, false>(p, acc, 0, 0, 0, 32, 0, threadIdx.x, s);\n}}\n}} }}\n')
+    flags = [f for f in build.HIPCC_FLAGS if f not in ("-shared", "-Wall")]
+    r = subprocess.run([build.hipcc(), *flags, "--cuda-device-only", "-fsyntax-only", "-I", build.INCLUDE, "-I", build.CSRC,
+                        str(use)], capture_output=True, text=True, timeout=300)
+    assert (r.returncode == 0) == fits, r.stderr[-2000:]
+    assert fits or "chunks a row" in r.stderr

@@ -334,7 +334,7 @@ template <int SCALE, int NI, int NJ, bool PAST>
 __device__ __forceinline__ void store_tile(const ProductArgs &p, floatx4 (&acc)[NI][NJ], int g, int64_t yoff,
                                            int64_t i0, int64_t i1, int64_t j0, int lane, char *scratch) {
     constexpr int CH = 2 * NJ, ROWS = 64 / CH;  // chunks of a row, rows a wave stores at once
-    static_assert((NJ & (NJ - 1)) == 0 && NJ >= 2 && NJ <= 16, "a power of two chunks a row");
+    static_assert((NJ & (NJ - 1)) == 0 && NJ >= 2 && NJ <= 8, "a power of two chunks a row, at most 16");
     const int l = lane & 15, q = lane >> 4;
     const bool f32 = p.ytype == BAKRON_T_F32;
     const int es = f32 ? 4 : 2, per = 16 / es;
