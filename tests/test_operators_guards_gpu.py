@@ -106,3 +106,48 @@ def test_bad_offsets_stay_inside(bk, call, form, rows, N, K, groups):
         want, mass = form(x, w), form(x.abs(), w.abs())
         got = Y[e * N:(e + 1) * N] if call == "grad_w" else Y[at[e]:at[e + 1]]
         assert bool(((got.double().cpu() - want).abs() <= 2.0 ** -8 * want.abs() + share * mass + 2.0 ** -24).all()), e
+
+
+@pytest.mark.parametrize("form,rows,N,K,groups", SHAPES, ids=[s[0] for s in SHAPES])
+@pytest.mark.parametrize("call", ["forward", "grad_x", "fp8 row", "fp8 block"])
+@pytest.mark.parametrize("left", [1, 0.6])
+def test_rows_of_no_group(bk, call, form, rows, N, K, groups, left):
+    """Rows after the last group's get 0, in every form; the others are as without them."""
+    if call == "grad_x":
+        N, K = K, N
+    rest = 1 if left == 1 else int(rows * left)
+    g = torch.Generator().manual_seed(rows + N * K)
+    at = np.linspace(0, rows - rest, groups + 1).astype(int)
+    at[1] = at[2] if groups > 2 else at[1]  # an empty group
+    off = torch.tensor(at, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    w = torch.randn(groups, N, K, generator=g).mul_(0.1).bfloat16().cuda()
+    x = torch.randn(rows, N if call == "grad_x" else K, generator=g).bfloat16().cuda()
+    Y = torch.full((rows, K if call == "grad_x" else N), 7.0, dtype=torch.bfloat16, device="cuda")
+    a, b = x.double().cpu(), w.double().cpu()
+    if call == "forward":
+        bk.grouped_matmul(x, w, off, out=Y, dev_status=status)
+    elif call == "grad_x":
+        Y, _ = bk.grouped_matmul_grad(x, Y, w, off, want_w=False, dev_status=status)
+    else:
+        x8, sx = bk.fp8_quantize(x)
+        w8, sw = bk.fp8_quantize(w.view(-1, K))
+        w8 = w8.view(groups, N, K)
+        if call == "fp8 row":
+            sw = torch.rand(groups, N, generator=g).add_(0.5).cuda()
+            scale = sw.double().cpu()[..., None]
+        else:
+            sw = torch.rand(groups, -(-K // 128), -(-N // 128), generator=g).add_(0.5).cuda()
+            scale = sw.double().cpu().transpose(1, 2).repeat_interleave(128, 1).repeat_interleave(128, 2)[:, :N, :K]
+        bk.fp8_matmul(x8, sx, w8, sw, off, out=Y, dev_status=status)
+        a = x8.double().cpu() * sx.double().cpu().t().repeat_interleave(128, 1)[:, :K]
+        b = w8.double().cpu() * scale
+    assert int(status) == 0
+    y = Y.double().cpu()
+    assert bool((y[rows - rest:] == 0).all())
+    length = N if call == "grad_x" else K
+    share = 2.0 ** -12 if call.startswith("fp8") else (length + 8) * 2.0 ** -23
+    for e in range(groups):
+        v, m = a[at[e]:at[e + 1]], b[e] if call == "grad_x" else b[e].T
+        want, mass = v @ m, v.abs() @ m.abs()
+        assert bool(((y[at[e]:at[e + 1]] - want).abs() <= 2.0 ** -8 * want.abs() + share * mass + 2.0 ** -24).all()), e
