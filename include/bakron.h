@@ -322,7 +322,7 @@ int32_t bakron_fp8_from_codes(const int8_t *codes, const float *zeros, int64_t m
  * the last at most rows) gives group g the rows offsets[g] .. offsets[g+1] - 1
  * of X and Y; groups may be empty.  Rows after the last group's get 0.  Offsets
  * that fall or leave [0, rows] set BAKRON_DEV_BAD_INDEX in *dev_status; nothing
- * outside the matrices is touched, and the result is undefined.  `offsets` NULL
+ * outside the matrices and the workspace is touched, and the result is undefined.  `offsets` NULL
  * goes with groups = 1: all rows.  The host never reads offsets.
  * Products are summed on the matrix cores in fp32; the order is fixed, so equal
  * inputs give equal bits.
