@@ -1,4 +1,4 @@
-"""What the products' hand-placed instructions rest on, checked in the assembly of this build.
+"""What the products' hand-placed instructions rest on, checked in the assembly that is compiled.
 
 The in-place products (v_mfma on accumulation registers) and the loads to LDS are inline
 assembly, whose hazards the compiler does not see.  The kernels keep clear of them only as

@@ -302,7 +302,7 @@ __device__ __forceinline__ floatx4 mfma(intx4 a, intx4 b, floatx4 c) {
 // moves accumulators about when they fill all 256 of these registers.  It does not
 // see the hazards of this form: settle() stands between other accesses of the
 // accumulators and these products, in both directions.  That nothing else comes too
-// close is checked in the assembly of each build (tests/test_products_assembly.py).
+// close is checked in the assembly that is compiled (tests/test_products_assembly.py).
 template <int ET>
 __device__ __forceinline__ void mfma_in_place(intx4 a, intx4 b, floatx4 &c) {
     if constexpr (ET == BAKRON_T_BF16)
