@@ -407,6 +407,60 @@ int32_t bakron_token_logprobs_grad(const void *logits, int32_t type, int64_t row
                                    const float *g_logprob, const float *g_entropy, void *dlogits,
                                    int64_t ldd, int32_t *dev_status, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Rows by group and back: what stands around a product by expert, or by adapter.
+ * A batch has `tokens` rows with k choices of a group each, hence n = tokens k pairs;
+ * pair t k + j is the j-th choice of token t.  n <= 2^24, k <= 64, groups <= 4096.
+ *
+ * bakron_group_sort -- a stable sort of the pairs by group:
+ *   ids      n group numbers, 32- or 64-bit (`id_bits`), contiguous.  A negative one
+ *            belongs to no group (a choice that was dropped, a row without adapter).
+ *            One >= groups is taken as negative and sets BAKRON_DEV_BAD_INDEX.
+ *   offsets  groups + 1 values: group g has the places offsets[g] .. offsets[g+1] - 1;
+ *            pairs of no group have those from offsets[groups] on.
+ *   order    n values: the pair at each place; pairs of one group keep their order
+ *   slots    n values: the place of each pair (order and slots are permutations, each
+ *            the other's inverse)
+ *   ws       bakron_group_sort_workspace_size() bytes
+ */
+size_t bakron_group_sort_workspace_size(int64_t n, int32_t groups);
+int32_t bakron_group_sort(const void *ids, int32_t id_bits, int64_t n, int32_t groups, int32_t *offsets,
+                          int32_t *order, int32_t *slots, int32_t *dev_status, void *ws, size_t ws_bytes,
+                          void *stream);
+
+/*
+ * The calls below take the slots (tokens x k, each place once) and offsets of a
+ * sort.  Of the offsets they read the last.  A slot outside [0, n) is left out and sets
+ * BAKRON_DEV_BAD_INDEX; a place that no slot names is not written.
+ *
+ * bakron_group_gather -- out[slots[t][j]] = X[t], and 0 for pairs of no group.
+ *   X tokens x cols, out n x cols, of one type.  The gradient of X is
+ *   bakron_group_combine of out's, without weights.
+ * bakron_group_gather_fp8 -- the same in e4m3 with a scale for each row and 128
+ *   columns, as bakron_fp8_quantize rounds (each token once).  Q n x cols, scales
+ *   ceil(cols / 128) x n; pairs of no group get codes 0 and scales 1.
+ * bakron_group_combine -- out[t] = sum_j weights[t][j] Y[slots[t][j]] over the choices
+ *   that have a group, in fp32, in the order of j, rounded once.  weights tokens x k
+ *   fp32, or NULL for 1.  Y n x cols, out tokens x cols, of one type.  Rows of Y of no
+ *   group are not read.
+ * bakron_group_combine_grad -- its gradients: dY[slots[t][j]] = weights[t][j] dout[t] (0
+ *   for pairs of no group), dweights[t][j] = <dout[t], Y[slots[t][j]]> (fp32, 0 for pairs
+ *   of no group).
+ */
+int32_t bakron_group_gather(const void *X, int32_t type, int64_t tokens, int32_t k, int64_t cols, int64_t ldx,
+                            const int32_t *slots, int32_t groups, const int32_t *offsets, void *out, int64_t ldo,
+                            int32_t *dev_status, void *stream);
+int32_t bakron_group_gather_fp8(const void *X, int32_t type, int64_t tokens, int32_t k, int64_t cols, int64_t ldx,
+                                const int32_t *slots, int32_t groups, const int32_t *offsets, uint8_t *Q,
+                                int64_t ldq, float *scales, int32_t *dev_status, void *stream);
+int32_t bakron_group_combine(const void *Y, int32_t type, int64_t tokens, int32_t k, int64_t cols, int64_t ldy,
+                             const int32_t *slots, int32_t groups, const int32_t *offsets, const float *weights,
+                             void *out, int64_t ldo, int32_t *dev_status, void *stream);
+int32_t bakron_group_combine_grad(const void *dout, int64_t ldd, const void *Y, int32_t type, int64_t tokens,
+                                  int32_t k, int64_t cols, int64_t ldy, const int32_t *slots, int32_t groups,
+                                  const int32_t *offsets, const float *weights, void *dY, int64_t lddy,
+                                  float *dweights, int32_t *dev_status, void *stream);
+
 const char *bakron_status_string(int32_t status);
 const char *bakron_last_error(void);
 

@@ -38,6 +38,8 @@ EXPORTS = (
     "bakron_grouped_matmul_workspace_size", "bakron_grouped_matmul", "bakron_grouped_matmul_grad_x",
     "bakron_grouped_matmul_grad_w",
     "bakron_token_logprobs_workspace_size", "bakron_token_logprobs", "bakron_token_logprobs_grad",
+    "bakron_group_sort_workspace_size", "bakron_group_sort", "bakron_group_gather", "bakron_group_gather_fp8",
+    "bakron_group_combine", "bakron_group_combine_grad",
     "bakron_status_string", "bakron_last_error",
 )
 
@@ -103,6 +105,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.bakron_token_logprobs.restype = I32
     lib.bakron_token_logprobs_grad.argtypes = [P, I32, I64, I64, I64, P, P, P, P, P, P, I64, P, P]
     lib.bakron_token_logprobs_grad.restype = I32
+    lib.bakron_group_sort_workspace_size.argtypes = [I64, I32]
+    lib.bakron_group_sort_workspace_size.restype = SZ
+    lib.bakron_group_sort.argtypes = [P, I32, I64, I32, P, P, P, P, P, SZ, P]
+    lib.bakron_group_sort.restype = I32
+    lib.bakron_group_gather.argtypes = [P, I32, I64, I32, I64, I64, P, I32, P, P, I64, P, P]
+    lib.bakron_group_gather.restype = I32
+    lib.bakron_group_gather_fp8.argtypes = [P, I32, I64, I32, I64, I64, P, I32, P, P, I64, P, P, P]
+    lib.bakron_group_gather_fp8.restype = I32
+    lib.bakron_group_combine.argtypes = [P, I32, I64, I32, I64, I64, P, I32, P, P, P, I64, P, P]
+    lib.bakron_group_combine.restype = I32
+    lib.bakron_group_combine_grad.argtypes = [P, I64, P, I32, I64, I32, I64, I64, P, I32, P, P, P, I64, P, P, P]
+    lib.bakron_group_combine_grad.restype = I32
     lib.bakron_status_string.argtypes = [I32]
     lib.bakron_status_string.restype = ctypes.c_char_p
     lib.bakron_last_error.argtypes = []
@@ -572,3 +586,136 @@ def token_logprobs_grad(logits, targets, lse, entropy, g_logprob, g_entropy=None
                                               D.data_ptr(), ldd, _status(dev_status), _here()),
                "bakron_token_logprobs_grad")
     return D
+
+
+# Rows by group and back.
+
+def group_sort(ids, groups, dev_status=None, stream=None):
+    """A stable sort of ids (int32 or int64, contiguous, negative: no group) by group
+    (bakron_group_sort).  Returns int32 tensors (offsets (groups + 1,), order (n,),
+    slots of ids' shape): group g has the places offsets[g] .. offsets[g + 1] - 1, order
+    is the element at each place, slots the place of each element.  Elements of no group
+    come last."""
+    if _elsewhere(stream):
+        return _on(stream, group_sort, ids, groups, dev_status)
+    lib = load()
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise BakronError(f"ids must be int32 or int64, not {ids.dtype}")
+    ip, n, dev = _vector(ids, "ids", ids.dtype, ids.shape), ids.numel(), ids.device
+    if not 1 <= groups <= 4096:
+        raise BakronError(f"groups must be in 1 .. 4096, not {groups}")
+    if n == 0:
+        return (torch.zeros(groups + 1, dtype=torch.int32, device=dev),
+                torch.empty(0, dtype=torch.int32, device=dev), torch.empty(ids.shape, dtype=torch.int32, device=dev))
+    offsets = torch.empty(groups + 1, dtype=torch.int32, device=dev)
+    order = torch.empty(n, dtype=torch.int32, device=dev)
+    slots = torch.empty(ids.shape, dtype=torch.int32, device=dev)
+    ws = _space(lib.bakron_group_sort_workspace_size(n, groups), dev)
+    _check(lib.bakron_group_sort(ip, 32 if ids.dtype == torch.int32 else 64, n, groups, offsets.data_ptr(),
+                                 order.data_ptr(), slots.data_ptr(), _status(dev_status),
+                                 None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _here()),
+           "bakron_group_sort")
+    return offsets, order, slots
+
+
+def _pairs(slots, offsets, tokens):
+    """(k, groups, slots' and offsets' pointers) after checks."""
+    if slots.dim() == 1:
+        k = 1
+    elif slots.dim() == 2 and slots.shape[1]:
+        k = slots.shape[1]
+    else:
+        raise BakronError(f"slots must be (tokens, k), not {tuple(slots.shape)}")
+    if slots.shape[0] != tokens:
+        raise BakronError(f"slots are of {slots.shape[0]} tokens, not {tokens}")
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise BakronError(f"offsets must be (groups + 1,), not {tuple(offsets.shape)}")
+    return (k, offsets.shape[0] - 1, _vector(slots, "slots", torch.int32, slots.shape),
+            _vector(offsets, "offsets", torch.int32, offsets.shape))
+
+
+def group_gather(X, slots, offsets, out=None, dev_status=None, stream=None):
+    """The rows of X (tokens, cols) copied to the places of a group_sort of (tokens, k)
+    choices, 0 for choices of no group (bakron_group_gather).  Returns (tokens k, cols).
+    The gradient of X is group_combine of the copies' gradients, without weights."""
+    if _elsewhere(stream):
+        return _on(stream, group_gather, X, slots, offsets, out, dev_status)
+    lib = load()
+    ldx = _rows_of(X, "X", _TYPES, empty=True)
+    tokens, cols = X.shape
+    k, groups, sp, op = _pairs(slots, offsets, tokens)
+    Y, ldo = _out(out, (tokens * k, cols), X.dtype, X.device, "out")
+    if tokens:
+        _check(lib.bakron_group_gather(X.data_ptr(), _TYPES[X.dtype], tokens, k, cols, ldx, sp, groups, op, Y.data_ptr(),
+                                       ldo, _status(dev_status), _here()), "bakron_group_gather")
+    return Y
+
+
+def group_gather_fp8(X, slots, offsets, out=None, scales=None, dev_status=None, stream=None):
+    """group_gather in e4m3 with a scale for each row and 128 columns, as fp8_matmul takes
+    them (bakron_group_gather_fp8).  Returns (codes (tokens k, cols), scales
+    (ceil(cols / 128), tokens k))."""
+    if _elsewhere(stream):
+        return _on(stream, group_gather_fp8, X, slots, offsets, out, scales, dev_status)
+    lib = load()
+    ldx = _rows_of(X, "X", _TYPES, empty=True)
+    tokens, cols = X.shape
+    k, groups, sp, op = _pairs(slots, offsets, tokens)
+    Q, ldq = _out(out, (tokens * k, cols), _FP8, X.device, "out")
+    of = (-(-cols // 128), tokens * k)
+    S = torch.empty(of, dtype=torch.float32, device=X.device) if scales is None else scales
+    cp = S.data_ptr() if scales is None else _vector(S, "scales", torch.float32, of)
+    if tokens:
+        _check(lib.bakron_group_gather_fp8(X.data_ptr(), _TYPES[X.dtype], tokens, k, cols, ldx, sp, groups, op,
+                                           Q.data_ptr(), ldq, cp, _status(dev_status), _here()),
+               "bakron_group_gather_fp8")
+    return Q, S
+
+
+def _combined(Y, slots, offsets, weights):
+    """(row distance, tokens, k, groups, pointers) of the sorted rows Y, after checks."""
+    ldy = _rows_of(Y, "Y", _TYPES, empty=True)
+    tokens = slots.shape[0] if slots.dim() else 0
+    k, groups, sp, op = _pairs(slots, offsets, tokens)
+    if Y.shape[0] != tokens * k:
+        raise BakronError(f"Y has {Y.shape[0]} rows, slots {tokens * k}")
+    return ldy, tokens, k, groups, sp, op, None if weights is None else _vector(weights, "weights", torch.float32,
+                                                                                slots.shape)
+
+
+def group_combine(Y, slots, offsets, weights=None, out=None, dev_status=None, stream=None):
+    """out[t] = sum_j weights[t][j] Y[slots[t][j]] over the choices that have a group
+    (bakron_group_combine).  Y (tokens k, cols); weights (tokens, k) in float32, or None
+    for 1.  Returns (tokens, cols) in Y's dtype."""
+    if _elsewhere(stream):
+        return _on(stream, group_combine, Y, slots, offsets, weights, out, dev_status)
+    lib = load()
+    ldy, tokens, k, groups, sp, op, wp = _combined(Y, slots, offsets, weights)
+    cols = Y.shape[1]
+    R, ldo = _out(out, (tokens, cols), Y.dtype, Y.device, "out")
+    if tokens:
+        _check(lib.bakron_group_combine(Y.data_ptr(), _TYPES[Y.dtype], tokens, k, cols, ldy, sp, groups, op, wp,
+                                        R.data_ptr(), ldo, _status(dev_status), _here()), "bakron_group_combine")
+    return R
+
+
+def group_combine_grad(dout, Y, slots, offsets, weights, out=None, dev_status=None, stream=None):
+    """group_combine's gradients (dY of Y's shape and dtype, dweights (tokens, k) in
+    float32) for dout (bakron_group_combine_grad); 0 for choices of no group."""
+    if _elsewhere(stream):
+        return _on(stream, group_combine_grad, dout, Y, slots, offsets, weights, out, dev_status)
+    lib = load()
+    if weights is None:
+        raise BakronError("weights are needed; without them Y's gradient is group_gather of dout")
+    ldy, tokens, k, groups, sp, op, wp = _combined(Y, slots, offsets, weights)
+    cols = Y.shape[1]
+    ldd = _rows_of(dout, "dout", (Y.dtype,), empty=True)
+    if dout.shape != (tokens, cols):
+        raise BakronError(f"dout must be of shape {(tokens, cols)}, not {tuple(dout.shape)}")
+    dY, lddy = _out(out, (tokens * k, cols), Y.dtype, Y.device, "out")
+    dw = torch.empty(slots.shape, dtype=torch.float32, device=Y.device)
+    if tokens:
+        _check(lib.bakron_group_combine_grad(dout.data_ptr(), ldd, Y.data_ptr(), _TYPES[Y.dtype], tokens, k, cols, ldy,
+                                             sp, groups, op, wp, dY.data_ptr(), lddy, dw.data_ptr(),
+                                             _status(dev_status), _here()), "bakron_group_combine_grad")
+    return dY, dw
