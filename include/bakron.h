@@ -461,6 +461,35 @@ int32_t bakron_group_combine_grad(const void *dout, int64_t ldd, const void *Y, 
                                   const int32_t *offsets, const float *weights, void *dY, int64_t lddy,
                                   float *dweights, int32_t *dev_status, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * bakron_verify_drafts -- which drafted tokens a target model keeps, and the token that
+ * follows them, from given random numbers; a rounded model drafts for its original.  Per
+ * request, with drafts d_i drawn from q_i and the target's probabilities p_i:
+ *   draft i is accepted where u_i q_i(d_i) < p_i(d_i) and all before it are;
+ *   at the first refusal the token is drawn from max(p_i - q_i, 0) (from p_i where that
+ *   has no weight), after the last draft from the p that follows: the first token whose
+ *   cumulated weight is above v times the whole.
+ * Products, differences and sums are in 64 bits.
+ *   p  batch x (drafts + 1) rows of vocab probabilities, row stride ldp
+ *   q  batch x drafts rows, row stride ldq; NULL where drafts were not drawn: then q(d_i)
+ *      counts as 1 and a refused token is left out of p_i
+ *      (both `type` BAKRON_T_*; rows need not sum to 1, only to be finite and >= 0)
+ *   draft_tokens  batch x drafts; a negative one ends a request's drafts
+ *   u batch x drafts, v batch: uniform in [0, 1), fp32
+ *   accepted  batch;  tokens  batch x (drafts + 1): the accepted drafts, the drawn token,
+ *             then -1
+ *   ws  *_workspace_size() bytes.  batch <= 2^20, drafts 0 .. 64, vocab <= 2^24.
+ * Rows after the first refusal are not read.  A draft >= vocab is refused and sets
+ * BAKRON_DEV_BAD_INDEX.  A NaN or an infinity of a p or q that was compared, and a sum of
+ * weights that is not finite, set BAKRON_DEV_NONFINITE; the drawn token is -1 for such a
+ * sum, and where a row of p has no weight at all.
+ */
+size_t bakron_verify_drafts_workspace_size(int64_t batch, int32_t drafts, int64_t vocab);
+int32_t bakron_verify_drafts(const void *p, int64_t ldp, const void *q, int64_t ldq, int32_t type, int64_t batch,
+                             int32_t drafts, int64_t vocab, const int64_t *draft_tokens, const float *u,
+                             const float *v, int32_t *accepted, int64_t *tokens, int32_t *dev_status, void *ws,
+                             size_t ws_bytes, void *stream);
+
 const char *bakron_status_string(int32_t status);
 const char *bakron_last_error(void);
 

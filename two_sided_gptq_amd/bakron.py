@@ -40,6 +40,7 @@ EXPORTS = (
     "bakron_token_logprobs_workspace_size", "bakron_token_logprobs", "bakron_token_logprobs_grad",
     "bakron_group_sort_workspace_size", "bakron_group_sort", "bakron_group_gather", "bakron_group_gather_fp8",
     "bakron_group_combine", "bakron_group_combine_grad",
+    "bakron_verify_drafts_workspace_size", "bakron_verify_drafts",
     "bakron_status_string", "bakron_last_error",
 )
 
@@ -117,6 +118,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.bakron_group_combine.restype = I32
     lib.bakron_group_combine_grad.argtypes = [P, I64, P, I32, I64, I32, I64, I64, P, I32, P, P, P, I64, P, P, P]
     lib.bakron_group_combine_grad.restype = I32
+    lib.bakron_verify_drafts_workspace_size.argtypes = [I64, I32, I64]
+    lib.bakron_verify_drafts_workspace_size.restype = SZ
+    lib.bakron_verify_drafts.argtypes = [P, I64, P, I64, I32, I64, I32, I64, P, P, P, P, P, P, P, SZ, P]
+    lib.bakron_verify_drafts.restype = I32
     lib.bakron_status_string.argtypes = [I32]
     lib.bakron_status_string.restype = ctypes.c_char_p
     lib.bakron_last_error.argtypes = []
@@ -586,6 +591,40 @@ def token_logprobs_grad(logits, targets, lse, entropy, g_logprob, g_entropy=None
                                               D.data_ptr(), ldd, _status(dev_status), _here()),
                "bakron_token_logprobs_grad")
     return D
+
+
+def verify_drafts(p, q, drafts, u, v, dev_status=None, stream=None):
+    """Which drafted tokens the target keeps, and the token after them (bakron_verify_drafts).
+
+    p (batch, n + 1, vocab) the target's probabilities; q (batch, n, vocab) the draft's, or
+    None for drafts that were not drawn from any; drafts (batch, n) int64, negative from a
+    request's end on; u (batch, n) and v (batch,) float32 in [0, 1).  Returns (accepted
+    (batch,) int32, tokens (batch, n + 1) int64: the accepted drafts, the drawn token, -1)."""
+    if _elsewhere(stream):
+        return _on(stream, verify_drafts, p, q, drafts, u, v, dev_status)
+    lib = load()
+    if p.dim() != 3 or drafts.dim() != 2 or p.shape[:2] != (drafts.shape[0], drafts.shape[1] + 1):
+        raise BakronError(f"p {tuple(p.shape)} and drafts {tuple(drafts.shape)} do not fit")
+    (batch, n), vocab, dev = drafts.shape, p.shape[2], p.device
+    if batch == 0:
+        return (torch.empty(0, dtype=torch.int32, device=dev), torch.empty((0, n + 1), dtype=torch.int64, device=dev))
+    ldp, ldq = _rows_of(p, "p", _TYPES, 3), 0
+    if n == 0:
+        q = None
+    if q is not None:
+        if q.shape != (batch, n, vocab):
+            raise BakronError(f"q must be of shape {(batch, n, vocab)}, not {tuple(q.shape)}")
+        ldq = _rows_of(q, "q", (p.dtype,), 3)
+    vectors = (_vector(drafts, "drafts", torch.int64, (batch, n)), _vector(u, "u", torch.float32, (batch, n)),
+               _vector(v, "v", torch.float32, (batch,)))
+    accepted = torch.empty(batch, dtype=torch.int32, device=dev)
+    tokens = torch.empty((batch, n + 1), dtype=torch.int64, device=dev)
+    ws = _space(lib.bakron_verify_drafts_workspace_size(batch, n, vocab), dev)
+    _check(lib.bakron_verify_drafts(p.data_ptr(), ldp, None if q is None else q.data_ptr(), ldq, _TYPES[p.dtype], batch, n,
+                                    vocab, *vectors, accepted.data_ptr(), tokens.data_ptr(), _status(dev_status),
+                                    None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _here()),
+           "bakron_verify_drafts")
+    return accepted, tokens
 
 
 # Rows by group and back.
