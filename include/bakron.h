@@ -462,6 +462,45 @@ int32_t bakron_group_combine_grad(const void *dout, int64_t ldd, const void *Y, 
                                   float *dweights, int32_t *dev_status, void *stream);
 
 /* ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection.  Places of a
+ * bakron_group_sort of the rows' adapters (k = 1): group g has the places offsets[g] ..
+ * offsets[g+1] - 1, order[place] is the row there (NULL: the place itself; each row once),
+ * rows from offsets[groups] on have no adapter.  offsets NULL goes with groups = 1.
+ * Offsets as for the products by group; an order outside [0, rows) is left out and sets
+ * BAKRON_DEV_BAD_INDEX.
+ *
+ * bakron_adapter_matmul -- out[r] = base[r] + scale_g B_g (A_g X[r]) for row r of adapter
+ * g, base[r] for a row without one
+ *   X  rows x K;  A  groups x rank x K;  B  groups x N x rank (A and B contiguous): bf16 or
+ *      fp16 (`type`).  rank 1 .. 256.
+ *   scale  groups fp32, or NULL for 1
+ *   base, out  rows x N of that type or fp32 (`otype`); base NULL counts as 0, and base
+ *      may be out: then rows without adapter are left as they are
+ *   ws  *_workspace_size() bytes
+ * Sums are in fp32.  The rank values between the two products keep 16 bits (a relative
+ * 2^-16), out is rounded once.
+ *
+ * bakron_adapter_matmul_grad -- for dY (rows x N), with U = scale dY B and
+ * P = scale X A^T:
+ *   dX = base + U A (base as above, of dX's type);  dA_g = U_g^T X_g;  dB_g = dY_g^T P_g
+ *   dX, dA and dB of the inputs' type or fp32 (`xtype`, `wtype`).  dX may be NULL, dA and dB
+ *   too (both; then X may be).  Adapters without rows get 0.
+ */
+size_t bakron_adapter_matmul_workspace_size(int64_t rows, int64_t N, int64_t K, int32_t rank, int32_t groups);
+int32_t bakron_adapter_matmul(const void *X, int32_t type, int64_t ldx, const void *A, const void *B, int64_t rows,
+                              int64_t N, int64_t K, int32_t rank, int32_t groups, const int32_t *offsets,
+                              const int32_t *order, const float *scale, const void *base, int64_t ldb, void *out,
+                              int32_t otype, int64_t ldo, int32_t *dev_status, void *ws, size_t ws_bytes,
+                              void *stream);
+size_t bakron_adapter_matmul_grad_workspace_size(int64_t rows, int64_t N, int64_t K, int32_t rank, int32_t groups);
+int32_t bakron_adapter_matmul_grad(const void *dY, int64_t lddy, const void *X, int32_t type, int64_t ldx,
+                                   const void *A, const void *B, int64_t rows, int64_t N, int64_t K, int32_t rank,
+                                   int32_t groups, const int32_t *offsets, const int32_t *order, const float *scale,
+                                   const void *base, int64_t ldb, void *dX, int32_t xtype, int64_t lddx, void *dA,
+                                   void *dB, int32_t wtype, int32_t *dev_status, void *ws, size_t ws_bytes,
+                                   void *stream);
+
+/* ---------------------------------------------------------------------------
  * bakron_verify_drafts -- which drafted tokens a target model keeps, and the token that
  * follows them, from given random numbers; a rounded model drafts for its original.  Per
  * request, with drafts d_i drawn from q_i and the target's probabilities p_i:

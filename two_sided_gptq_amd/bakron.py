@@ -40,6 +40,8 @@ EXPORTS = (
     "bakron_token_logprobs_workspace_size", "bakron_token_logprobs", "bakron_token_logprobs_grad",
     "bakron_group_sort_workspace_size", "bakron_group_sort", "bakron_group_gather", "bakron_group_gather_fp8",
     "bakron_group_combine", "bakron_group_combine_grad",
+    "bakron_adapter_matmul_workspace_size", "bakron_adapter_matmul",
+    "bakron_adapter_matmul_grad_workspace_size", "bakron_adapter_matmul_grad",
     "bakron_verify_drafts_workspace_size", "bakron_verify_drafts",
     "bakron_status_string", "bakron_last_error",
 )
@@ -118,6 +120,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.bakron_group_combine.restype = I32
     lib.bakron_group_combine_grad.argtypes = [P, I64, P, I32, I64, I32, I64, I64, P, I32, P, P, P, I64, P, P, P]
     lib.bakron_group_combine_grad.restype = I32
+    lib.bakron_adapter_matmul_workspace_size.argtypes = [I64, I64, I64, I32, I32]
+    lib.bakron_adapter_matmul_workspace_size.restype = SZ
+    lib.bakron_adapter_matmul.argtypes = [P, I32, I64, P, P, I64, I64, I64, I32, I32, P, P, P, P, I64, P, I32, I64, P, P,
+                                          SZ, P]
+    lib.bakron_adapter_matmul.restype = I32
+    lib.bakron_adapter_matmul_grad_workspace_size.argtypes = [I64, I64, I64, I32, I32]
+    lib.bakron_adapter_matmul_grad_workspace_size.restype = SZ
+    lib.bakron_adapter_matmul_grad.argtypes = [P, I64, P, I32, I64, P, P, I64, I64, I64, I32, I32, P, P, P, P, I64, P, I32,
+                                               I64, P, P, I32, P, P, SZ, P]
+    lib.bakron_adapter_matmul_grad.restype = I32
     lib.bakron_verify_drafts_workspace_size.argtypes = [I64, I32, I64]
     lib.bakron_verify_drafts_workspace_size.restype = SZ
     lib.bakron_verify_drafts.argtypes = [P, I64, P, I64, I32, I64, I32, I64, P, P, P, P, P, P, P, SZ, P]
@@ -758,3 +770,104 @@ def group_combine_grad(dout, Y, slots, offsets, weights, out=None, dev_status=No
                                              sp, groups, op, wp, dY.data_ptr(), lddy, dw.data_ptr(),
                                              _status(dev_status), _here()), "bakron_group_combine_grad")
     return dY, dw
+
+
+# Low-rank adapters beside a shared projection.
+
+def _adapters(A, B, offsets, order, scale, rows, dtype):
+    """(N, K, rank, groups, pointers of A, B, offsets, order, scale) after checks."""
+    if A.dim() not in (2, 3) or B.dim() != A.dim() or A.shape[:-2] != B.shape[:-2] or A.shape[-2] != B.shape[-1] or \
+            A.numel() == 0 or B.numel() == 0:
+        raise BakronError(f"A {tuple(A.shape)} and B {tuple(B.shape)} do not fit")
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise BakronError(f"X, A and B must be bfloat16 or float16, not {dtype}")
+    groups, op = _groups(A, offsets)
+    return (B.shape[-2], A.shape[-1], A.shape[-2], groups, _vector(A, "A", dtype, A.shape), _vector(B, "B", dtype, B.shape),
+            op, None if order is None else _vector(order, "order", torch.int32, (rows,)),
+            None if scale is None else _vector(scale, "scale", torch.float32, (groups,)))
+
+
+def _added(base, out, shape, dtype, want, device):
+    """(out, its row distance, base's pointer and row distance): base is of out's dtype, `want`
+    or the inputs' dtype."""
+    if base is not None:
+        if want is not None and base.dtype != want:
+            raise BakronError(f"base must be {want}, not {base.dtype}")
+        want = base.dtype
+    want = dtype if want is None and out is None else out.dtype if want is None else want
+    if want not in (dtype, torch.float32):
+        raise BakronError(f"the output's dtype must be {dtype} or float32, not {want}")
+    Y, ldo = _out(out, shape, want, device, "out")
+    if base is None:
+        return Y, ldo, None, 0
+    if base.shape != shape:
+        raise BakronError(f"base must be of shape {tuple(shape)}, not {tuple(base.shape)}")
+    return Y, ldo, base.data_ptr(), _rows_of(base, "base", (want,), empty=True)
+
+
+def adapter_matmul(X, A, B, offsets=None, order=None, scale=None, base=None, out=None, out_dtype=None, dev_status=None,
+                   stream=None):
+    """out[r] = base[r] + scale_g B_g (A_g X[r]) with each row's adapter g (bakron_adapter_matmul).
+
+    X (rows, K); A (adapters, rank, K) and B (adapters, N, rank), contiguous, or without the
+    first dimension for one adapter; all bfloat16 or float16.  offsets and order: group_sort
+    of the rows' adapters (order None: rows lie sorted); scale (adapters,) float32 or None.
+    base (rows, N), the shared projection's result, of out's dtype, which is X's or float32;
+    None counts as 0.  out may be base."""
+    if _elsewhere(stream):
+        return _on(stream, adapter_matmul, X, A, B, offsets, order, scale, base, out, out_dtype, dev_status)
+    lib = load()
+    ldx = _rows_of(X, "X", (torch.bfloat16, torch.float16), empty=True)
+    rows = X.shape[0]
+    N, K, rank, groups, ap, bp, op, rp, cp = _adapters(A, B, offsets, order, scale, rows, X.dtype)
+    if X.shape[1] != K:
+        raise BakronError(f"X's rows have {X.shape[1]} elements, A's {K}")
+    Y, ldo, base_p, ldb = _added(base, out, (rows, N), X.dtype, out_dtype, X.device)
+    if rows == 0:
+        return Y
+    ws = _space(lib.bakron_adapter_matmul_workspace_size(rows, N, K, rank, groups), X.device)
+    _check(lib.bakron_adapter_matmul(X.data_ptr(), _TYPES[X.dtype], ldx, ap, bp, rows, N, K, rank, groups, op, rp, cp,
+                                     base_p, ldb, Y.data_ptr(), _TYPES[Y.dtype], ldo, _status(dev_status),
+                                     None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _here()),
+           "bakron_adapter_matmul")
+    return Y
+
+
+def adapter_matmul_grad(dY, X, A, B, offsets=None, order=None, scale=None, base=None, out=None, want_x=True, want_w=True,
+                        x_dtype=None, w_dtype=None, dev_status=None, stream=None):
+    """adapter_matmul's gradients (dX, dA, dB) for dY (rows, N) (bakron_adapter_matmul_grad).
+    dX is added to base, the gradient that X gets from the shared projection (None: 0), and
+    written to out if given (it may be base).  Those that are not wanted are None.  x_dtype
+    and w_dtype: X's (the default) or float32."""
+    if _elsewhere(stream):
+        return _on(stream, adapter_matmul_grad, dY, X, A, B, offsets, order, scale, base, out, want_x, want_w, x_dtype,
+                   w_dtype, dev_status)
+    lib = load()
+    lddy = _rows_of(dY, "dY", (torch.bfloat16, torch.float16), empty=True)
+    ldx = _rows_of(X, "X", (dY.dtype,), empty=True)
+    rows, dtype, dev = X.shape[0], X.dtype, X.device
+    N, K, rank, groups, ap, bp, op, rp, cp = _adapters(A, B, offsets, order, scale, rows, dtype)
+    if dY.shape != (rows, N) or X.shape[1] != K:
+        raise BakronError(f"dY {tuple(dY.shape)}, X {tuple(X.shape)}, A and B do not fit")
+    dX, lddx, base_p, ldb, dA, dB = None, 0, None, 0, None, None
+    if want_x:
+        dX, lddx, base_p, ldb = _added(base, out, (rows, K), dtype, x_dtype, dev)
+    elif base is not None or out is not None:
+        raise BakronError("base and out go with want_x")
+    if want_w:
+        w_dtype = dtype if w_dtype is None else w_dtype
+        if w_dtype not in (dtype, torch.float32):
+            raise BakronError(f"w_dtype must be {dtype} or float32, not {w_dtype}")
+        new = torch.zeros if rows == 0 else torch.empty
+        dA, dB = (new(t.shape, dtype=w_dtype, device=dev) for t in (A, B))
+    if rows == 0 or not (want_x or want_w):
+        return dX, dA, dB
+    ws = _space(lib.bakron_adapter_matmul_grad_workspace_size(rows, N, K, rank, groups), dev)
+    _check(lib.bakron_adapter_matmul_grad(dY.data_ptr(), lddy, X.data_ptr(), _TYPES[dtype], ldx, ap, bp, rows, N, K, rank,
+                                          groups, op, rp, cp, base_p, ldb, None if dX is None else dX.data_ptr(),
+                                          _TYPES[dtype if dX is None else dX.dtype], lddx,
+                                          None if dA is None else dA.data_ptr(), None if dB is None else dB.data_ptr(),
+                                          _TYPES[w_dtype] if want_w else 0, _status(dev_status),
+                                          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _here()),
+           "bakron_adapter_matmul_grad")
+    return dX, dA, dB

@@ -15,7 +15,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbakron.so")
 
 SOURCES = ["common.hip", "quantize.hip", "hessian.hip", "factor.hip", "fp8.hip", "products.hip",
-           "logprobs.hip", "groups.hip", "drafts.hip"]
+           "logprobs.hip", "groups.hip", "drafts.hip", "adapters.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
