@@ -99,42 +99,54 @@ struct Groups {
     int32_t *dev_status;
 };
 
-__device__ __forceinline__ int wave_scan(int x) {
+// The slot-th tile of `high` places, counted group by group (rows of no group last).
+// before: how many tiles of `small` places the groups before it have, where asked for.
+// most > 0: slots of groups are dealt so that neighbouring tiles, which share a group's
+// matrices, share an XCD's L2; slot becomes the tile's number.  Only tiles that exist are
+// dealt, or the last XCDs would have none, and no more than `most`, for which the
+// workspace is sized: offsets that fall can make more.  Wave uniform.
+__device__ __forceinline__ Tile tile_of(const Groups &a, int high, int &slot, int most, int small = 0,
+                                        int *before = nullptr) {
     const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int y = __shfl_up(x, off);
-        if (lane >= off) x += y;
+    int64_t p, z;
+    auto tiles_of = [&](int g) {
+        p = z = 0;
+        if (g <= a.groups) rows_of_group(a.offsets, a.groups, a.rows, g, p, z);
+        return ((int)(z - p) + high - 1) / high;
+    };
+    int mine = tiles_of(lane), upto = wave_scan(mine), sum = 0;
+    if (most > 0) {
+        int all = __builtin_amdgcn_readlane(upto, min(a.groups - 1, 63));
+        if (a.groups > 64) {
+            for (int base = 64; base < a.groups; base += 64)
+                all += __builtin_amdgcn_readlane(wave_scan(base + lane < a.groups ? tiles_of(base + lane) : 0), 63);
+            mine = tiles_of(lane);
+        }
+        all = min(all, most);
+        if (slot < all) slot = (int)xcd_order(slot, all);
     }
-    return x;
-}
-
-// The slot-th tile of `high` places, counted group by group (rows of no group last); before:
-// how many tiles of `small` places the groups before it have.  Wave uniform.
-__device__ __forceinline__ Tile tile_of(const Groups &a, int high, int slot, int small, int &before) {
-    const int lane = threadIdx.x & 63;
-    before = 0;
-    for (int base = 0; base <= a.groups; base += 64) {
-        int64_t p = 0, z = 0;
-        if (base + lane <= a.groups) rows_of_group(a.offsets, a.groups, a.rows, base + lane, p, z);
-        const int mine = (int)((z - p + high - 1) / high), fine = (int)((z - p + small - 1) / small);
-        const int upto = wave_scan(mine), fine_upto = wave_scan(fine);
-        const uint64_t hit = __ballot(slot < upto);
+    int left = slot;
+    for (int base = 0;;) {
+        const int fine = before ? ((int)(z - p) + small - 1) / small : 0, fine_upto = before ? wave_scan(fine) : 0;
+        const uint64_t hit = __ballot(left < upto);
         if (hit) {
             const int src = __ffsll((unsigned long long)hit) - 1;
             Tile t;
             t.g = base + src;
             const int first = __builtin_amdgcn_readlane((int)p, src), end = __builtin_amdgcn_readlane((int)z, src);
-            t.p0 = first + (slot - __builtin_amdgcn_readlane(upto - mine, src)) * high;
+            t.p0 = first + (left - __builtin_amdgcn_readlane(upto - mine, src)) * high;
             t.p1 = min(end, t.p0 + high);
             t.pad = 0;
-            before += __builtin_amdgcn_readlane(fine_upto - fine, src);
+            if (before) *before = sum + __builtin_amdgcn_readlane(fine_upto - fine, src);
             return t;
         }
-        slot -= __builtin_amdgcn_readlane(upto, 63);
-        before += __builtin_amdgcn_readlane(fine_upto, 63);
+        left -= __builtin_amdgcn_readlane(upto, 63);
+        if (before) sum += __builtin_amdgcn_readlane(fine_upto, 63);
+        base += 64;
+        if (base > a.groups) return {-1, 0, 0, 0};
+        mine = tiles_of(base + lane);
+        upto = wave_scan(mine);
     }
-    return {-1, 0, 0, 0};
 }
 
 // The row at a place; -1 past the tile and for one that is out of range.
@@ -162,9 +174,9 @@ __device__ __forceinline__ void report(const Groups &a, const Tile &t, bool firs
 
 // One product of each of the two that a gradient needs: blockIdx.z.
 struct Shrink {
-    const char *x, *w;      // rows of K values; rank rows of K values a group
-    int64_t ldx, ldw, group_w;
-    int K;
+    const char *x, *w;      // rows of K values; a group's matrix
+    int64_t ldx, group_w;
+    int K, strided;         // the matrix is rank x K (0) or K x rank (1)
     uint32_t *by_place;     // [16-place tile][16][ranks], or NULL
     uint32_t *by_rank;      // [16-place tile][ranks][16], or NULL
 };
@@ -173,89 +185,174 @@ struct ShrinkArgs {
     Shrink job[2];
     const float *scale;     // of a group, or NULL
     int rank, ranks;        // ranks: in whole 16s
+    int high, slots;        // places of a tile, tiles
     Tile *tiles;            // written by the first job
 };
 
 // The least tile is for few rows: its workgroup streams K with as many waves as fit.
 constexpr int shrink_waves(int mt, int rt) { return mt == 1 && rt == 1 ? 16 : 8; }
+constexpr int SHRINK_STEP = 64;  // values of K
+constexpr int shrink_lds(int mt, int rt) {
+    const int through = 16 * SHRINK_STEP * 2, sums = mt * rt * 1024;
+    return shrink_waves(mt, rt) * (through > sums ? through : sums);
+}
 
-template <int T, int MT, int RT>
-__global__ __launch_bounds__(64 * shrink_waves(MT, RT)) void shrink_kernel(ShrinkArgs a) {
+// GRAD: matrices of either order.
+template <int T, int MT, int RT, bool GRAD>
+__global__ __launch_bounds__(64 * shrink_waves(MT, RT), GRAD && MT * RT == 8 ? 2 : 4) void shrink_kernel(ShrinkArgs a) {
     extern __shared__ __align__(16) float space[];
     const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
-    constexpr int waves = shrink_waves(MT, RT);
+    constexpr int waves = shrink_waves(MT, RT), KS = SHRINK_STEP, DEPTH = MT * RT == 1 ? 3 : MT * RT == 2 ? 2 : 1;
+    constexpr int CH = KS / 8, PER = 64 / CH, NL = 16 / PER;  // chunks of a row; rows of a load, loads of 16 rows
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int slot = blockIdx.x, r0 = blockIdx.y * RT * 16;
+    const int parts = a.high / (16 * MT), r0 = blockIdx.y * RT * 16;
+    // the parts of a tile lie 8 apart, on one XCD
+    const int block = blockIdx.x, sub = (block >> 3) % parts * MT;
+    int slot = (block >> 3) / parts * 8 + (block & 7);
+    if (slot >= a.slots) return;
     const Shrink &job = a.job[blockIdx.z];
-    int before;
-    const Tile t = tile_of(a.of, 16 * MT, slot, 16 * MT, before);
-    if (blockIdx.y == 0 && blockIdx.z == 0) {
+    Tile t = tile_of(a.of, a.high, slot, a.slots);
+    if (blockIdx.y == 0 && blockIdx.z == 0 && sub == 0) {
         if (threadIdx.x == 0) a.tiles[slot] = t;
-        report(a.of, t, slot == 0);
+        report(a.of, t, block == 0);
     }
-    if (t.g < 0 || t.g == a.of.groups) return;
+    t.p0 += sub * 16;
+    if (t.g < 0 || t.g == a.of.groups || t.p0 >= t.p1) return;
+    // Loads go by neighbouring lanes along a row, KS values of it: 16 lanes of a load that lie in
+    // 16 rows, as the matrix cores want them, take 16 cycles for 256 bytes instead of 4 (64
+    // rows, K = 16384: 31 against 13 us).  A step's 16 rows pass through LDS of the wave's own,
+    // 16-byte chunk c of row r at place c ^ r.
     // Places past the tile and ranks past the last read a row that exists; their results
     // are not used.
-    const char *x[MT], *m[RT];
-    bool valid[MT];
+    const int lr = lane / CH, lc = lane % CH;
+    const char *m = job.w + 2 * t.g * job.group_w, *x[MT][NL];
+    const bool strided = GRAD && job.strided, whole_ranks = a.rank % 8 == 0;
+    const uint32_t wide = (uint32_t)job.K * 2, narrow = (uint32_t)a.rank * 2;
+    // 16 ranks of a step.  rank x K: as the rows of X.  K x rank: a lane has one of the 64 rows.
+    auto load_w = [&](int s, int j, uintx4(&gm)[NL]) {
+        int from = r0 + j * 16;
+        asm("" : "+s"(from));  // addresses are made anew: there are no registers for all of them
+        if (!strided) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int row = row_at(a.of, t.p0 + i * 16 + l, t.p1);
-        valid[i] = row >= 0;
-        x[i] = job.x + 2 * max(row, 0) * job.ldx;
-    }
+            for (int h = 0; h < NL; ++h)
+                gm[h] = load_whole(m + lc * 16 + (uint64_t)wide * (uint32_t)min(from + lr + h * PER, a.rank - 1), s * KS);
+        } else {
 #pragma unroll
-    for (int i = 0; i < RT; ++i) m[i] = job.w + 2 * (t.g * job.group_w + min(r0 + i * 16 + l, a.rank - 1) * job.ldw);
+            for (int h = 0; h < NL; ++h) {
+                const char *row = m + (uint64_t)narrow * (uint32_t)(s * KS + lane);
+                const int r = from + h * 8;
+                gm[h] = whole_ranks ? load_whole(row, min(r, a.rank - 8)) : load_frag(row, r, a.rank - r);
+            }
+        }
+    };
+    auto load_w_tail = [&](int k, int j, uintx4(&gm)[NL]) {
+#pragma unroll
+        for (int h = 0; h < NL; ++h) {
+            const int r = r0 + j * 16 + h * 8;
+            if (!strided)
+                gm[h] = load_frag(m + (uint64_t)wide * (uint32_t)min(r0 + j * 16 + lr + h * PER, a.rank - 1), k + lc * 8,
+                                  job.K - k - lc * 8);
+            else
+                gm[h] = load_frag(m + (uint64_t)narrow * (uint32_t)min(k + lane, job.K - 1), r, k + lane < job.K ? a.rank - r : 0);
+        }
+    };
     floatx4 acc[MT][RT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < RT; ++j) acc[i][j] = floatx4{0, 0, 0, 0};
-    // 64 of K a step: a wave reads whole lines
-    const int whole = job.K / 64;
-    uintx4 fx[2][MT], fm[2][RT];
-    auto load = [&](int s) {
+    // KS of K a step, DEPTH steps on their way.  Workgroups begin at different columns: rows of
+    // a power of two in bytes would otherwise have all of them at the same memory channels.
+    const int whole = job.K / KS, turned = whole ? (int)((int64_t)blockIdx.x * waves % whole) : 0;
+    auto step = [&](int s) { return s + turned < whole ? s + turned : s + turned - whole; };
+    uintx4 vx[DEPTH][MT][NL], vm[DEPTH][RT][NL];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int k = s * 64 + h * 32 + q * 8;
+    for (int d = 0; d < DEPTH; ++d)
+        if (w + d * waves < whole)
 #pragma unroll
-            for (int i = 0; i < MT; ++i) fx[h][i] = load_whole(x[i], k);
+            for (int j = 0; j < RT; ++j) load_w(step(w + d * waves), j, vm[d][j]);
+    int row[MT];
 #pragma unroll
-            for (int j = 0; j < RT; ++j) fm[h][j] = load_whole(m[j], k);
+    for (int i = 0; i < MT; ++i) {
+        row[i] = row_at(a.of, t.p0 + i * 16 + l, t.p1);
+#pragma unroll
+        for (int h = 0; h < NL; ++h) x[i][h] = job.x + 2 * (max(__shfl(row[i], h * PER + lr), 0) * job.ldx + lc * 8);
+    }
+    auto load_x = [&](int s, int i, uintx4(&gx)[NL]) {
+#pragma unroll
+        for (int h = 0; h < NL; ++h) gx[h] = load_whole(x[i][h], s * KS);
+    };
+    char *own = reinterpret_cast<char *>(space) + w * (16 * KS * 2);
+    auto through = [&](const uintx4(&v)[NL], uintx4(&f)[NL]) {
+#pragma unroll
+        for (int h = 0; h < NL; ++h) {
+            const int r = h * PER + lr;
+            *reinterpret_cast<uintx4 *>(own + r * (KS * 2) + (lc ^ (r & (CH - 1))) * 16) = v[h];
+        }
+#pragma unroll
+        for (int h = 0; h < NL; ++h)
+            f[h] = *reinterpret_cast<const uintx4 *>(own + l * (KS * 2) + ((h * 4 + q) ^ (l & (CH - 1))) * 16);
+    };
+    // K x rank: rows of 32 bytes, read with a transposing load: lane l of 16 gets rank l and 4
+    // of K from each.
+    auto through_strided = [&](const uintx4(&v)[NL], uintx4(&f)[NL]) {
+        typedef short shortx4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) shortx4 *lds4;
+#pragma unroll
+        for (int h = 0; h < NL; ++h) *reinterpret_cast<uintx4 *>(own + lane * 32 + h * 16) = v[h];
+#pragma unroll
+        for (int h = 0; h < NL; ++h) {
+            char *at = own + (h * 32 + q * 8 + (l >> 2)) * 32 + (l & 3) * 8;
+            const shortx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at));
+            const shortx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at + 4 * 32));
+            __builtin_memcpy(&f[h], &lo, 8);
+            __builtin_memcpy(reinterpret_cast<char *>(&f[h]) + 8, &hi, 8);
         }
     };
-    auto multiply = [&](const uintx4(&gx)[2][MT], const uintx4(&gm)[2][RT]) {
+    // Registers take the loads of step `next` as soon as LDS has what they held.
+    auto multiply = [&](uintx4(&gx)[MT][NL], uintx4(&gm)[RT][NL], int next) {
+        uintx4 fx[MT][NL];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int i = 0; i < MT; ++i) {
+            through(gx[i], fx[i]);
+            if (next < whole) load_x(step(next), i, gx[i]);
+        }
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+        for (int j = 0; j < RT; ++j) {
+            uintx4 fm[NL];
+            if (strided)
+                through_strided(gm[j], fm);
+            else
+                through(gm[j], fm);
+            if (next < whole) load_w(step(next), j, gm[j]);
 #pragma unroll
-                for (int j = 0; j < RT; ++j) acc[i][j] = mfma<T>(gx[h][i], gm[h][j], acc[i][j]);
+            for (int h = 0; h < NL; ++h)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) acc[i][j] = mfma<T>(fx[i][h], fm[h], acc[i][j]);
+        }
     };
-    if (w < whole) load(w);
-    for (int s = w; s < whole; s += waves) {
-        uintx4 gx[2][MT], gm[2][RT];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+    for (int d = 0; d < DEPTH; ++d)
+        if (w + d * waves < whole)
 #pragma unroll
-            for (int i = 0; i < MT; ++i) gx[h][i] = fx[h][i];
+            for (int i = 0; i < MT; ++i) load_x(step(w + d * waves), i, vx[d][i]);
+    for (int s = w; s < whole; s += DEPTH * waves) {
 #pragma unroll
-            for (int j = 0; j < RT; ++j) gm[h][j] = fm[h][j];
-        }
-        if (s + waves < whole) load(s + waves);
-        multiply(gx, gm);
+        for (int d = 0; d < DEPTH; ++d)
+            if (s + d * waves < whole) multiply(vx[d], vm[d], s + (d + DEPTH) * waves);
     }
-    if (whole * 64 < job.K && w == whole % waves) {
+    if (whole * KS < job.K && w == whole % waves) {
+        const int k = whole * KS, left = job.K - k - lc * 8;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int k = whole * 64 + h * 32 + q * 8;
+        for (int h = 0; h < NL; ++h) {
 #pragma unroll
-            for (int i = 0; i < MT; ++i) fx[h][i] = load_frag(x[i], k, job.K - k);
-#pragma unroll
-            for (int j = 0; j < RT; ++j) fm[h][j] = load_frag(m[j], k, job.K - k);
+            for (int i = 0; i < MT; ++i) vx[0][i][h] = load_frag(x[i][h], k, left);
         }
-        multiply(fx, fm);
+#pragma unroll
+        for (int j = 0; j < RT; ++j) load_w_tail(k, j, vm[0][j]);
+        multiply(vx[0], vm[0], whole);
     }
+    __syncthreads();
     // the waves' sums, in order
     floatx4 *sums = reinterpret_cast<floatx4 *>(space);
 #pragma unroll
@@ -273,12 +370,12 @@ __global__ __launch_bounds__(64 * shrink_waves(MT, RT)) void shrink_kernel(Shrin
             floatx4 s = sums[c * waves * 64 + lane];
             for (int v = 1; v < waves; ++v) s += sums[(c * waves + v) * 64 + lane];
             // lane: rank l, places 4 q ..
-            const int64_t tile = (int64_t)slot * MT + i;
+            const int64_t tile = (int64_t)slot * (a.high / 16) + sub + i;
             const int rank = r0 + j * 16 + l;
             uintx4 packed;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const bool ok = __shfl((int)valid[i], q * 4 + e) && rank < a.rank;
+                const bool ok = __shfl(row[i], q * 4 + e) >= 0 && rank < a.rank;
                 packed[e] = ok ? pack_parts(s[e] * scale) : 0;
             }
             if (job.by_rank) *reinterpret_cast<uintx4 *>(job.by_rank + (tile * a.ranks + rank) * 16 + q * 4) = packed;
@@ -294,138 +391,259 @@ struct ExpandArgs {
     Groups of;
     const Tile *tiles;
     const uint32_t *p;      // [16-place tile][16][ranks]
-    const char *w;          // N rows of `rank` values a group
-    int64_t group_w, ldw;
+    const char *w;          // a group's matrix
+    int64_t group_w;        // STRIDED: rank x N, else N x rank
     const char *base;       // may be out; NULL: 0
     char *out;
     int64_t ldb, ldo;
-    int N, rank, ranks, turns;  // turns: 64-column pieces of a wave
+    int N, rank, ranks;
+    int per_chunk;          // 2^16 / (rank / 8), rounded up: divides what is below 2^11
 };
 
-// 16 consecutive elements.
+// 8 elements as they are, of a 16-bit type or fp32.
 template <int T>
-__device__ __forceinline__ void load16(const char *base, int64_t i, int left, float *x) {
-    load8<T>(base, i, left, x);
-    load8<T>(base, i + 8, left - 8, x + 8);
-}
-template <int T>
-__device__ __forceinline__ void store16(char *base, int64_t i, int left, const float *x) {
-    store8<T>(base, i, left, x);
-    store8<T>(base, i + 8, left - 8, x + 8);
-}
+struct Raw8 {
+    uint32_t w[T == BAKRON_T_F32 ? 8 : 4];
+};
 
 // D = W P^T with W's rows as the first operand: a lane then holds 4 of W's rows (columns of
-// out) for one place.  The 64 columns of a piece are dealt to 4 products so that those are 16
-// neighbours: row m of product t is column (m / 4) 16 + 4 t + m % 4.
-template <int T, int OT, int MT, int RS>
-__global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
-    const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int pieces = (a.N + 63) / 64, per = 4 * a.turns, blocks = (pieces + per - 1) / per;
-    const int64_t slot = blockIdx.x / blocks;
-    const int block = (int)(blockIdx.x - slot * blocks);
-    const Tile t = a.tiles[slot];
-    if (t.g < 0) return;
+// out) for one place.  A workgroup takes a tile's places and 256 columns, a wave 64 of
+// them: W's part stays in registers, P in LDS.
+//
+// All that is in memory is read and written along rows by neighbouring lanes (see
+// shrink_kernel), and passes through LDS of the wave's own to and from the lanes that the
+// matrix cores want it in.  All loads are on their way before the first is waited for.
+// Needs 256 columns and, where W is N x rank, ranks in whole 8s.
+template <int T>
+__device__ __forceinline__ void add_products(const uintx4 &f, const uintx4 &hi, const uintx4 &lo, floatx4 &acc) {
+    if constexpr (T == BAKRON_T_BF16) {
+        acc = mfma_bf16(f, lo, mfma_bf16(f, hi, acc));
+    } else {
+        uintx4 fh, fl;
+        split_f16(f, fh, fl);
+        acc = mfma_bf16(fh, lo, mfma_bf16(fh, hi, acc));
+        acc = mfma_bf16(fl, lo, mfma_bf16(fl, hi, acc));
+    }
+}
+
+// P of the tile's places to LDS, rows of `ranks` 4 words apart.
+__device__ __forceinline__ void stage_p(const ExpandArgs &a, int64_t sub, int count, uint32_t *lds) {
+    const uint32_t *p = a.p + sub * 16 * a.ranks;
+    const int words = (count + 15) / 16 * 16 * a.ranks;
+    for (int i = threadIdx.x * 4; i < words; i += 1024) {
+        const int r = i / a.ranks, c = i - r * a.ranks;
+        *reinterpret_cast<uintx4 *>(lds + r * (a.ranks + 4) + c) = *reinterpret_cast<const uintx4 *>(p + i);
+    }
+}
+
+__device__ __forceinline__ void p_frags(const ExpandArgs &a, const uint32_t *lds, int place, int r, uintx4 &hi, uintx4 &lo) {
+    uint32_t p[8] = {};
+    if (r < a.ranks) __builtin_memcpy(p, __builtin_assume_aligned(lds + place * (a.ranks + 4) + r, 16), 32);
+    unpack_parts(p, hi, lo);
+}
+
+constexpr int EXPAND_ROW = 68;  // floats between the rows of results in LDS
+
+template <int T, int OT, int MT, int RS, bool STRIDED>
+__device__ __forceinline__ void expand_whole(const ExpandArgs &a, const Tile &t, int64_t slot, int n0, uint32_t *lds, char *own) {
+    constexpr int OS = OT == BAKRON_T_F32 ? 4 : 2;
+    constexpr int PER = RS == 1 ? 4 : 1;          // 16-row pieces of W that pass at a time
+    constexpr int WL = RS == 1 ? 4 : 2 * RS / 2;  // loads of a pass
+    const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4, lr = lane >> 3, lc = lane & 7;
     const bool none = t.g == a.of.groups;
-    if (none && a.base == a.out) return;
-    int row[MT];
-    uintx4 hi[MT][RS], lo[MT][RS];
+    const int count = t.p1 - t.p0;
+    int row[MT][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) row[i][h] = row_at(a.of, t.p0 + i * 16 + h * 8 + lr, t.p1);
+    const int chunks = a.rank / 8, some = 16 * PER * chunks;  // 16-byte pieces of a row, of a pass
+    const char *wg = a.w + 2 * ((none ? 0 : t.g) * a.group_w);
+    uintx4 raw_w[4 * RS];
+    if constexpr (!STRIDED) {
+        // W's 64 rows are one stretch of memory
+        wg += 2 * (int64_t)n0 * a.rank;
+#pragma unroll
+        for (int c = 0; c < 4 / PER; ++c)
+#pragma unroll
+            for (int k = 0; k < WL; ++k)
+                if (k * 64 + lane < some) raw_w[c * WL + k] = load_whole(wg, (int64_t)(c * some + k * 64 + lane) * 8);
+    } else {
+        // 64 columns of all ranks, 8 rows a load
+        wg += 2 * (n0 + lc * 8);
+#pragma unroll
+        for (int k = 0; k < 4 * RS; ++k) {
+            raw_w[k] = uintx4{0, 0, 0, 0};
+            if (k * 8 < a.rank) {
+                raw_w[k] = load_whole(wg, (int64_t)min(k * 8 + lr, a.rank - 1) * a.N);
+                if (k * 8 + lr >= a.rank) raw_w[k] = uintx4{0, 0, 0, 0};
+            }
+        }
+    }
+    // places without a row read row 0 and write nothing
+    Raw8<OT> base[MT][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            base[i][h] = Raw8<OT>{};
+            if (a.base) __builtin_memcpy(base[i][h].w, a.base + OS * (max(row[i][h], 0) * a.ldb + n0 + lc * 8), 8 * OS);
+        }
+    if (!none) stage_p(a, slot * MT, count, lds);
+    __syncthreads();
+    uintx4 f[4][RS];
+    if constexpr (!STRIDED) {
+#pragma unroll
+        for (int c = 0; c < 4; c += PER) {
+#pragma unroll
+            for (int k = 0; k < WL; ++k) {
+                const int i = k * 64 + lane, r = i * a.per_chunk >> 16;  // i / chunks
+                if (i < some) *reinterpret_cast<uintx4 *>(own + (i + r) * 16) = raw_w[c / PER * WL + k];
+            }
+#pragma unroll
+            for (int d = 0; d < PER; ++d)
+#pragma unroll
+                for (int s = 0; s < RS; ++s) {
+                    f[c + d][s] = uintx4{0, 0, 0, 0};
+                    if (s * 4 + q < chunks)
+                        f[c + d][s] = *reinterpret_cast<const uintx4 *>(own + ((d * 16 + l) * (chunks + 1) + s * 4 + q) * 16);
+                }
+        }
+    } else {
+        // rows of 128 bytes, the 32 of 16 columns at place c ^ (row & 3), read with a transposing load
+        typedef short shortx4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) shortx4 *lds4;
+#pragma unroll
+        for (int s = 0; s < RS; ++s) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = k * 8 + lr;
+                *reinterpret_cast<uintx4 *>(own + r * 128 + (((lc >> 1) ^ (r & 3)) * 32) + (lc & 1) * 16) = raw_w[s * 4 + k];
+            }
+            const int r = q * 8 + (l >> 2);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                char *at = own + r * 128 + (c ^ (r & 3)) * 32 + (l & 3) * 8;
+                const shortx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at));
+                const shortx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at + 4 * 128));
+                __builtin_memcpy(&f[c][s], &lo, 8);
+                __builtin_memcpy(reinterpret_cast<char *>(&f[c][s]) + 8, &hi, 8);
+            }
+        }
+    }
+    float *results = reinterpret_cast<float *>(own);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-        row[i] = row_at(a.of, t.p0 + i * 16 + l, t.p1);
+        if (i * 16 >= count) break;
+        floatx4 acc[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[c] = floatx4{0, 0, 0, 0};
+        if (!none) {
+#pragma unroll
+            for (int s = 0; s < RS; ++s) {
+                uintx4 hi, lo;
+                p_frags(a, lds, i * 16 + l, s * 32 + q * 8, hi, lo);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) add_products<T>(f[c][s], hi, lo, acc[c]);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) *reinterpret_cast<floatx4 *>(results + l * EXPAND_ROW + c * 16 + q * 4) = acc[c];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float y[8];
+            unpack8<OT>(base[i][h].w, y);
+            if (!none) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const floatx4 d = *reinterpret_cast<const floatx4 *>(results + (h * 8 + lr) * EXPAND_ROW + lc * 8 + e * 4);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[e * 4 + k] += d[k];
+                }
+            }
+            if (row[i][h] >= 0) store8<OT>(a.out, row[i][h] * a.ldo + n0 + lc * 8, 8, y);
+        }
+    }
+}
+
+// The same for any N and rank: lanes read and write where the matrix cores have them.  The 64
+// columns are dealt to the 4 products so that a lane's are two runs of 8: row m of product
+// c is column 32 (c / 2) + 8 (m / 4) + 4 (c % 2) + m % 4.
+template <int T, int OT, int MT, int RS, bool STRIDED>
+__device__ __forceinline__ void expand_any(const ExpandArgs &a, const Tile &t, int64_t slot, int n0, uint32_t *lds) {
+    const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
+    const bool none = t.g == a.of.groups;
+    const int count = t.p1 - t.p0, col = n0 + q * 8, left = a.N - col;
+    uintx4 f[4][RS];
+    const char *wg = a.w + 2 * ((none ? 0 : t.g) * a.group_w);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int n = min(n0 + (c >> 1) * 32 + (l >> 2) * 8 + (c & 1) * 4 + (l & 3), a.N - 1);
 #pragma unroll
         for (int s = 0; s < RS; ++s) {
             const int r = s * 32 + q * 8;
-            uint32_t p[8] = {};
-            if (!none && r < a.ranks) __builtin_memcpy(p, a.p + ((slot * MT + i) * 16 + l) * a.ranks + r, 32);
-            unpack_parts(p, hi[i][s], lo[i][s]);
+            if constexpr (!STRIDED) {
+                f[c][s] = load_frag(wg, (int64_t)n * a.rank + r, a.rank - r);
+            } else {
+                f[c][s] = uintx4{0, 0, 0, 0};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (r + e < a.rank)
+                        f[c][s][e / 2] |= (uint32_t) reinterpret_cast<const uint16_t *>(wg)[(int64_t)(r + e) * a.N + n] << (16 * (e & 1));
+            }
         }
     }
-    for (int turn = 0; turn < a.turns; ++turn) {
-        const int n0 = ((block * a.turns + turn) * 4 + w) * 64;
-        if (n0 >= a.N) return;
-        floatx4 acc[MT][4];
+    if (!none) stage_p(a, slot * MT, count, lds);
+    __syncthreads();
+    for (int i = 0; i * 16 < count; ++i) {
+        const int row = row_at(a.of, t.p0 + i * 16 + l, t.p1);
+        float y[2][8] = {};
+        if (a.base && row >= 0)
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+            for (int h = 0; h < 2; ++h) load8<OT>(a.base, row * a.ldb + col + 32 * h, left - 32 * h, y[h]);
+        if (!none) {
+            floatx4 acc[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) acc[i][c] = floatx4{0, 0, 0, 0};
-        const int col = n0 + q * 16, left = a.N - col;
-        float y[MT][16];
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            if (a.base && row[i] >= 0) {
-                load16<OT>(a.base, row[i] * a.ldb + col, left, y[i]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) y[i][e] = 0.0f;
-            }
-        }
-        if (!none)
+            for (int c = 0; c < 4; ++c) acc[c] = floatx4{0, 0, 0, 0};
 #pragma unroll
             for (int s = 0; s < RS; ++s) {
-                const int r = s * 32 + q * 8;
+                uintx4 hi, lo;
+                p_frags(a, lds, i * 16 + l, s * 32 + q * 8, hi, lo);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int n = min(n0 + (l >> 2) * 16 + c * 4 + (l & 3), a.N - 1);
-                    const uintx4 f = load_frag(a.w, t.g * a.group_w + n * a.ldw + r, a.rank - r);
-                    if constexpr (T == BAKRON_T_BF16) {
-#pragma unroll
-                        for (int i = 0; i < MT; ++i)
-                            acc[i][c] = mfma_bf16(f, lo[i][s], mfma_bf16(f, hi[i][s], acc[i][c]));
-                    } else {
-                        uintx4 fh, fl;
-                        split_f16(f, fh, fl);
-#pragma unroll
-                        for (int i = 0; i < MT; ++i) {
-                            acc[i][c] = mfma_bf16(fh, lo[i][s], mfma_bf16(fh, hi[i][s], acc[i][c]));
-                            acc[i][c] = mfma_bf16(fl, lo[i][s], mfma_bf16(fl, hi[i][s], acc[i][c]));
-                        }
-                    }
-                }
+                for (int c = 0; c < 4; ++c) add_products<T>(f[c][s], hi, lo, acc[c]);
             }
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            if (row[i] < 0) continue;
-            if (!none)
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[i][c * 4 + e] += acc[i][c][e];
-            store16<OT>(a.out, row[i] * a.ldo + col, left, y[i]);
+                for (int e = 0; e < 4; ++e) y[c >> 1][(c & 1) * 4 + e] += acc[c][e];
         }
+        if (row >= 0)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) store8<OT>(a.out, row * a.ldo + col + 32 * h, left - 32 * h, y[h]);
     }
 }
 
-// ---------------------------------------------------------------- transposes
+// LDS of a workgroup: P, and what passes through for each wave.
+__host__ __device__ constexpr int expand_p_words(int mt, int ranks) { return 16 * mt * (ranks + 4); }
+__host__ __device__ constexpr int expand_own_bytes(int rank) {
+    // W as N x rank; as rank x N 4 KB, less than the results
+    const int w = (rank <= 32 ? 64 : 16) * (rank / 8 + 1) * 16, results = 16 * EXPAND_ROW * 4;
+    return w > results ? w : results;
+}
 
-// The gradients contract over the other dimension of A and B: rows x cols of each group
-// that has rows, to cols x rows.
-struct Transpose {
-    const char *from;
-    int64_t ld, group;
-    char *to;
-    int rows, cols;
-};
-struct TransposeArgs {
-    Groups of;
-    Transpose job[2];
-};
-__global__ __launch_bounds__(256) void transpose_kernel(TransposeArgs a) {
-    __shared__ uint16_t tile[64][65];
-    const Transpose &job = a.job[blockIdx.z];
-    const int g = blockIdx.y, across = (job.cols + 63) / 64, down = (job.rows + 63) / 64;
-    int64_t p, z;
-    rows_of_group(a.of.offsets, a.of.groups, a.of.rows, g, p, z);
-    if (p == z || blockIdx.x >= (unsigned)(across * down)) return;
-    const int r0 = blockIdx.x / across * 64, c0 = blockIdx.x % across * 64;
-    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-    const uint16_t *from = reinterpret_cast<const uint16_t *>(job.from) + g * job.group;
-    uint16_t *to = reinterpret_cast<uint16_t *>(job.to) + (int64_t)g * job.rows * job.cols;
-    for (int r = y; r < 64; r += 4)
-        if (r0 + r < job.rows && c0 + x < job.cols) tile[r][x] = from[(r0 + r) * job.ld + c0 + x];
-    __syncthreads();
-    for (int c = y; c < 64; c += 4)
-        if (c0 + c < job.cols && r0 + x < job.rows) to[(int64_t)(c0 + c) * job.rows + r0 + x] = tile[x][c];
+template <int T, int OT, int MT, int RS, bool STRIDED>
+__global__ __launch_bounds__(256) void expand_kernel(ExpandArgs a) {
+    extern __shared__ __align__(16) uint32_t lds[];
+    const int blocks = (a.N + 255) / 256;
+    const int64_t slot = blockIdx.x / blocks;
+    const int first = (int)(blockIdx.x - slot * blocks) * 256, n0 = first + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 64;
+    const Tile t = a.tiles[slot];
+    if (t.g < 0 || (t.g == a.of.groups && a.base == a.out)) return;
+    if ((STRIDED || a.rank % 8 == 0) && first + 256 <= a.N)
+        expand_whole<T, OT, MT, RS, STRIDED>(a, t, slot, n0, lds, reinterpret_cast<char *>(lds + expand_p_words(MT, a.ranks)) +
+                                                            (threadIdx.x >> 6) * expand_own_bytes(a.rank));
+    else
+        expand_any<T, OT, MT, RS, STRIDED>(a, t, slot, n0, lds);
 }
 
 // ---------------------------------------------------------------- outer
@@ -469,88 +687,106 @@ __device__ __forceinline__ void store_any1(char *base, int type, int64_t i, floa
         store1<BAKRON_T_F16>(base, i, x);
 }
 
-// A workgroup takes a unit's places, 128 columns and 16 RT ranks; its 4 waves share the
+// A workgroup takes a unit's places, 128 columns and 16 RT ranks; its waves share the
 // places, 32 at a time.  A lane reads 8 columns of 8 rows and turns them about with byte
 // permutes: the matrix cores want 8 places of one column.
-template <int T, int RT>
-__global__ __launch_bounds__(256) void outer_kernel(OuterArgs a) {
-    __shared__ __align__(16) floatx4 space[2 * 8 * RT * 64];
-    const Outer &job = a.job[blockIdx.z];
+constexpr int OUTER_WAVES = 8;
+
+template <int T, int RT, bool WHOLE>
+__device__ __forceinline__ void outer_sum(const OuterArgs &a, const Outer &job, const Tile &t, int64_t sub, int c0, int r0,
+                                          floatx4 (&acc)[8][RT]) {
     const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int across = (job.cols + 127) / 128;
-    const int unit = blockIdx.x % a.units, c0 = (blockIdx.x / a.units) * 128, r0 = blockIdx.y * RT * 16;
-    if (c0 >= across * 128) return;
-    Tile t;
-    int before;
-    if (a.chunk) {
-        t = tile_of(a.of, a.chunk, unit, a.high, before);
-        if (t.g < 0 || t.g == a.of.groups) return;
-    } else {
-        // all of group `unit`, also an empty one
-        int64_t p, z;
-        rows_of_group(a.of.offsets, a.of.groups, a.of.rows, unit, p, z);
-        t = {unit, (int)p, (int)z, 0};
-        before = 0;
-        int sum = 0;
-        for (int e = lane; e < unit; e += 64) {
-            int64_t p2, z2;
-            rows_of_group(a.of.offsets, a.of.groups, a.of.rows, e, p2, z2);
-            sum += (int)((z2 - p2 + a.high - 1) / a.high);
-        }
-        before = __builtin_amdgcn_readlane(wave_scan(sum), 63);
-    }
-    int64_t p, z;
-    rows_of_group(a.of.offsets, a.of.groups, a.of.rows, t.g, p, z);
-    // shrink's 16-place tiles of this unit
-    const int64_t sub = (int64_t)before * (a.high / 16) + (t.p0 - (int)p) / 16;
-    const int col = c0 + l * 8, left = job.cols - col;
-    floatx4 acc[8][RT];
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-#pragma unroll
-        for (int r = 0; r < RT; ++r) acc[c][r] = floatx4{0, 0, 0, 0};
-    for (int s = w * 32; s < t.p1 - t.p0; s += 128) {
+    const int col = c0 + l * 8, left = job.cols - col, count = t.p1 - t.p0;
+    // the rows of the next 32 places, one a lane
+    int next = row_at(a.of, t.p0 + w * 32 + (lane & 31), t.p1);
+    for (int s = w * 32; s < count; s += OUTER_WAVES * 32) {
+        const int row = next;
+        next = row_at(a.of, t.p0 + s + OUTER_WAVES * 32 + (lane & 31), t.p1);
         uintx4 v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int row = row_at(a.of, t.p0 + s + q * 8 + e, t.p1);
-            v[e] = row >= 0 ? load_frag(job.z, row * job.ldz + col, left) : uintx4{0, 0, 0, 0};
+            const int r = __shfl(row, q * 8 + e);
+            const int64_t at = max(r, 0) * job.ldz + col;
+            if constexpr (WHOLE)
+                v[e] = load_whole(job.z, at);
+            else
+                v[e] = load_frag(job.z, at, r >= 0 ? left : 0);
         }
-        uintx4 gh[RT], gl[RT];
+        uint32_t g[RT][8];
         const int64_t tile = sub + s / 16 + (q >> 1);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-            uint32_t g[8] = {};
             const int rank = r0 + r * 16 + l;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) g[r][k] = 0;
             // past the unit's last 16-place tile there is none (nor where offsets fall)
-            if (rank < a.ranks && tile >= 0 && tile < a.subs && t.p0 + s + (q & 2) * 8 < t.p1)
-                __builtin_memcpy(g, job.g + (tile * a.ranks + rank) * 16 + (q & 1) * 8, 32);
-            unpack_parts(g, gh[r], gl[r]);
+            if (rank < a.ranks && tile >= 0 && tile < a.subs && s + (q & 2) * 8 < count)
+                __builtin_memcpy(g[r], job.g + (tile * a.ranks + rank) * 16 + (q & 1) * 8, 32);
         }
+        // places without a row: what was read from row 0 does not count
+        if (WHOLE && __any(row < 0)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (__shfl(row, q * 8 + e) < 0) v[e] = uintx4{0, 0, 0, 0};
+        }
+        uintx4 gh[RT], gl[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) unpack_parts(g[r], gh[r], gl[r]);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             uintx4 f;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 f[j] = __builtin_amdgcn_perm(v[2 * j + 1][c / 2], v[2 * j][c / 2], c & 1 ? 0x07060302 : 0x05040100);
-            if constexpr (T == BAKRON_T_BF16) {
 #pragma unroll
-                for (int r = 0; r < RT; ++r) acc[c][r] = mfma_bf16(f, gl[r], mfma_bf16(f, gh[r], acc[c][r]));
-            } else {
-                uintx4 fh, fl;
-                split_f16(f, fh, fl);
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    acc[c][r] = mfma_bf16(fh, gl[r], mfma_bf16(fh, gh[r], acc[c][r]));
-                    acc[c][r] = mfma_bf16(fl, gl[r], mfma_bf16(fl, gh[r], acc[c][r]));
-                }
-            }
+            for (int r = 0; r < RT; ++r) add_products<T>(f, gh[r], gl[r], acc[c][r]);
         }
     }
-    // waves 2 and 3 to 0 and 1, then 1 to 0
+}
+
+template <int T, int RT>
+__global__ __launch_bounds__(64 * OUTER_WAVES) void outer_kernel(OuterArgs a) {
+    __shared__ __align__(16) floatx4 space[OUTER_WAVES / 2 * 8 * RT * 64];
+    const Outer &job = a.job[blockIdx.z];
+    const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wide = (max(a.job[0].cols, a.job[1].cols) + 127) / 128;
+    const int unit = blockIdx.x / wide, c0 = ((int)blockIdx.x - unit * wide) * 128, r0 = blockIdx.y * RT * 16;
+    if (c0 >= job.cols) return;
+    Tile t;
+    int before;
+    int64_t p, z;
+    if (a.chunk) {
+        int at = unit;
+        t = tile_of(a.of, a.chunk, at, 0, a.high, &before);
+        if (t.g < 0 || t.g == a.of.groups) return;
+        rows_of_group(a.of.offsets, a.of.groups, a.of.rows, t.g, p, z);
+    } else {
+        // all of group `unit`, also an empty one
+        int sum = 0;
+        for (int e = lane; e < unit; e += 64) {
+            rows_of_group(a.of.offsets, a.of.groups, a.of.rows, e, p, z);
+            sum += ((int)(z - p) + a.high - 1) / a.high;
+        }
+        before = __builtin_amdgcn_readlane(wave_scan(sum), 63);
+        rows_of_group(a.of.offsets, a.of.groups, a.of.rows, unit, p, z);
+        t = {unit, (int)p, (int)z, 0};
+    }
+    // shrink's 16-place tiles of this unit
+    const int64_t sub = (int64_t)before * (a.high / 16) + (t.p0 - (int)p) / 16;
+    floatx4 acc[8][RT];
 #pragma unroll
-    for (int half = 2; half > 0; half >>= 1) {
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[c][r] = floatx4{0, 0, 0, 0};
+    if (c0 + 128 <= job.cols)
+        outer_sum<T, RT, true>(a, job, t, sub, c0, r0, acc);
+    else
+        outer_sum<T, RT, false>(a, job, t, sub, c0, r0, acc);
+    // the upper half of the waves to the lower, until one is left
+#pragma unroll
+    for (int half = OUTER_WAVES / 2; half > 0; half >>= 1) {
         if (w >= half && w < 2 * half)
 #pragma unroll
             for (int c = 0; c < 8; ++c)
@@ -609,12 +845,16 @@ __global__ __launch_bounds__(256) void outer_join_kernel(OuterArgs a) {
     if (i >= (int64_t)a.rank * per_row) return;
     const int rank = (int)(i / per_row), col = (int)(i - (int64_t)rank * per_row) * 8, left = job.cols - col;
     float sum[8] = {};
-    for (int u = first; u < last; ++u) {
-        float x[8];
-        load8<BAKRON_T_F32>(reinterpret_cast<const char *>(a.part), u * a.part_size + job.part0 + (int64_t)rank * job.cols + col,
-                            left, x);
+    const char *from = reinterpret_cast<const char *>(a.part + job.part0 + (int64_t)rank * job.cols + col);
+    for (int u0 = first; u0 < last; u0 += 4) {
+        float x[4][8] = {};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] += x[e];
+        for (int k = 0; k < 4; ++k)
+            if (u0 + k < last) load8<BAKRON_T_F32>(from, (u0 + k) * a.part_size, left, x[k]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += x[k][e];
     }
     if (!job.by_column) {
         store_any(job.out, a.otype, g * job.group_o + rank * job.ldo + col, left, sum);
@@ -628,29 +868,33 @@ __global__ __launch_bounds__(256) void outer_join_kernel(OuterArgs a) {
 
 // How a call is laid out; the same for workspace and launch.
 struct Layout {
-    int mt, rt;             // shrink: 16-place tiles and 16-rank blocks of a workgroup
+    int mt;                 // 16-place tiles of a tile of expand: 1 or 4
+    int rt;                 // 16-rank blocks of a workgroup of shrink
     int ranks, rs;          // ranks in whole 16s; 32-rank steps of expand
     int64_t slots;          // tiles of 16 mt places
     int chunk;              // of the sums over places; 0: a group is one unit
     int64_t units;
 };
 
+// Places that a workgroup of shrink takes, in 16s.
+int shrink_mt(const Layout &y) { return y.mt == 1 ? 1 : 2; }
+
 Layout layout_of(int64_t rows, int64_t N, int64_t K, int32_t rank, int32_t groups, bool grad) {
     Layout y;
     y.ranks = (int)round_up(rank, 16);
     y.rs = rank <= 32 ? 1 : rank <= 64 ? 2 : rank <= 128 ? 4 : 8;
-    y.mt = rows >= 64 * (int64_t)(groups + 1) && rows >= 1024 ? 2 : 1;
+    y.mt = rows >= 64 * (int64_t)(groups + 1) && rows >= 1024 ? 4 : 1;
     y.slots = row_tiles(16 * y.mt, rows, groups, true);
     const int blocks = y.ranks / 16;
-    y.rt = y.slots * blocks <= 1024 ? 1 : blocks >= 4 ? 4 : blocks >= 2 ? 2 : 1;
+    y.rt = y.mt == 1 && y.slots * blocks <= 1024 ? 1 : blocks >= 4 ? 4 : blocks >= 2 ? 2 : 1;
     y.chunk = 0;
     y.units = groups;
     if (grad) {
-        const int64_t tiles = (N + 127) / 128 + (K + 127) / 128, want = 1024;
+        const int64_t tiles = (N + 127) / 128 + (K + 127) / 128, want = 512;
         if (tiles * groups < want && rows > 512) {
             const int64_t splits = (want + tiles - 1) / tiles;
             y.chunk = (int)round_up((rows + splits - 1) / splits, 128);
-            if (y.chunk < 256) y.chunk = 256;
+            if (y.chunk < 512) y.chunk = 512;
             y.units = row_tiles(y.chunk, rows, groups, true);
         }
     }
@@ -661,13 +905,16 @@ size_t place_words(const Layout &y) { return (size_t)y.slots * y.mt * 16 * y.ran
 
 template <int T, int MT, int RT>
 void launch_shrink(const ShrinkArgs &a, const Layout &y, int jobs, hipStream_t s) {
-    const dim3 grid((unsigned)y.slots, (unsigned)((y.ranks / 16 + RT - 1) / RT), jobs);
-    hipLaunchKernelGGL((shrink_kernel<T, MT, RT>), grid, dim3(64 * shrink_waves(MT, RT)),
-                       (size_t)shrink_waves(MT, RT) * MT * RT * 1024, s, a);
+    const dim3 grid((unsigned)(round_up(y.slots, 8) * (y.mt / MT)), (unsigned)((y.ranks / 16 + RT - 1) / RT), jobs);
+    if (a.job[0].strided)
+        hipLaunchKernelGGL((shrink_kernel<T, MT, RT, true>), grid, dim3(64 * shrink_waves(MT, RT)), shrink_lds(MT, RT), s, a);
+    else
+        hipLaunchKernelGGL((shrink_kernel<T, MT, RT, false>), grid, dim3(64 * shrink_waves(MT, RT)), shrink_lds(MT, RT), s, a);
 }
 template <int T>
-void launch_shrink(const ShrinkArgs &a, const Layout &y, int jobs, hipStream_t s) {
-    if (y.mt == 1) {
+void launch_shrink(ShrinkArgs a, const Layout &y, int jobs, hipStream_t s) {
+    a.high = 16 * y.mt, a.slots = (int)y.slots;
+    if (shrink_mt(y) == 1) {
         if (y.rt == 1) return launch_shrink<T, 1, 1>(a, y, jobs, s);
         if (y.rt == 2) return launch_shrink<T, 1, 2>(a, y, jobs, s);
         return launch_shrink<T, 1, 4>(a, y, jobs, s);
@@ -677,33 +924,25 @@ void launch_shrink(const ShrinkArgs &a, const Layout &y, int jobs, hipStream_t s
     launch_shrink<T, 2, 4>(a, y, jobs, s);
 }
 
-int expand_turns(const Layout &y, int64_t N) {
-    const int64_t pieces = (N + 63) / 64;
-    int turns = 1;
-    while (turns < 4 && y.slots * ((pieces + 8 * turns - 1) / (8 * turns)) >= 2048) turns *= 2;
-    return turns;
-}
-int64_t expand_blocks(const Layout &y, int64_t N, int turns) { return y.slots * (((N + 63) / 64 + 4 * turns - 1) / (4 * turns)); }
-
-template <int T, int OT, int MT>
+template <int T, int OT, int MT, bool STRIDED>
 void launch_expand(const ExpandArgs &a, const Layout &y, hipStream_t s) {
-    const dim3 grid((unsigned)expand_blocks(y, a.N, a.turns));
+    const dim3 grid((unsigned)(y.slots * ((a.N + 255) / 256)));
+    const size_t lds = expand_p_words(MT, y.ranks) * 4 + 4 * expand_own_bytes(a.rank);
     if (y.rs == 1)
-        hipLaunchKernelGGL((expand_kernel<T, OT, MT, 1>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((expand_kernel<T, OT, MT, 1, STRIDED>), grid, dim3(256), lds, s, a);
     else if (y.rs == 2)
-        hipLaunchKernelGGL((expand_kernel<T, OT, MT, 2>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((expand_kernel<T, OT, MT, 2, STRIDED>), grid, dim3(256), lds, s, a);
     else if (y.rs == 4)
-        hipLaunchKernelGGL((expand_kernel<T, OT, MT, 4>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((expand_kernel<T, OT, MT, 4, STRIDED>), grid, dim3(256), lds, s, a);
     else
-        hipLaunchKernelGGL((expand_kernel<T, OT, MT, 8>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((expand_kernel<T, OT, MT, 8, STRIDED>), grid, dim3(256), lds, s, a);
 }
-template <int T>
-void launch_expand(ExpandArgs a, int32_t otype, const Layout &y, hipStream_t s) {
-    a.turns = expand_turns(y, a.N);
+template <int T, bool STRIDED>
+void launch_expand(const ExpandArgs &a, int32_t otype, const Layout &y, hipStream_t s) {
     if (otype == BAKRON_T_F32)
-        y.mt == 1 ? launch_expand<T, BAKRON_T_F32, 1>(a, y, s) : launch_expand<T, BAKRON_T_F32, 2>(a, y, s);
+        y.mt == 1 ? launch_expand<T, BAKRON_T_F32, 1, STRIDED>(a, y, s) : launch_expand<T, BAKRON_T_F32, 4, STRIDED>(a, y, s);
     else
-        y.mt == 1 ? launch_expand<T, T, 1>(a, y, s) : launch_expand<T, T, 2>(a, y, s);
+        y.mt == 1 ? launch_expand<T, T, 1, STRIDED>(a, y, s) : launch_expand<T, T, 4, STRIDED>(a, y, s);
 }
 
 template <int T>
@@ -712,11 +951,11 @@ void launch_outer(const OuterArgs &a, const Layout &y, hipStream_t s) {
     const int blocks = y.ranks / 16;
     const unsigned x = (unsigned)(across * a.units);
     if (blocks == 1)
-        hipLaunchKernelGGL((outer_kernel<T, 1>), dim3(x, 1, 2), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((outer_kernel<T, 1>), dim3(x, 1, 2), dim3(64 * OUTER_WAVES), 0, s, a);
     else if (blocks == 2)
-        hipLaunchKernelGGL((outer_kernel<T, 2>), dim3(x, 1, 2), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((outer_kernel<T, 2>), dim3(x, 1, 2), dim3(64 * OUTER_WAVES), 0, s, a);
     else
-        hipLaunchKernelGGL((outer_kernel<T, 4>), dim3(x, (unsigned)((blocks + 3) / 4), 2), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((outer_kernel<T, 4>), dim3(x, (unsigned)((blocks + 3) / 4), 2), dim3(64 * OUTER_WAVES), 0, s, a);
     if (a.chunk) {
         const int64_t threads = a.rank * across * 16;
         hipLaunchKernelGGL(outer_join_kernel, dim3((unsigned)((threads + 255) / 256), a.of.groups, 2), dim3(256), 0, s, a);
@@ -730,7 +969,7 @@ bool sizes_ok(int64_t rows, int64_t N, int64_t K, int32_t rank, int32_t groups) 
           rank <= MAX_RANK && groups >= 1 && groups <= MAX_GROUPS))
         return false;
     // no launch of 2^32 threads or more: the widest tiles' first dimension, in all of them
-    const int64_t most = std::max(N, K), slots = row_tiles(16, rows, groups, true);
+    const int64_t most = std::max(N, K), slots = row_tiles(16, rows, groups, true) + 8;
     return slots * 1024 <= LAUNCH_THREADS && slots * ((most + 255) / 256) * 256 <= LAUNCH_THREADS &&
            std::max<int64_t>(groups, 1024 + groups + 1) * ((most + 127) / 128) * 256 <= LAUNCH_THREADS &&
            ((most + 63) / 64) * ((rank + 63) / 64) * 256 <= LAUNCH_THREADS;
@@ -767,11 +1006,10 @@ int32_t check_ws(const void *ws, size_t have, size_t need) {
     return BAKRON_ERR_WORKSPACE;
 }
 
-size_t grad_size(const Layout &y, int64_t N, int64_t K, int32_t rank, int32_t groups, bool x, bool w) {
+size_t grad_size(const Layout &y, int64_t N, int64_t K, int32_t rank, bool x, bool w) {
     size_t n = align256(y.slots * sizeof(Tile));
-    n += align256((size_t)groups * rank * N * 2);                           // B^T
-    if (x) n += align256((size_t)groups * rank * K * 2) + align256(place_words(y) * 4);  // A^T, U by place
-    if (w) n += 2 * align256(place_words(y) * 4);                           // U and P by rank
+    if (x) n += align256(place_words(y) * 4);      // U by place
+    if (w) n += 2 * align256(place_words(y) * 4);  // U and P by rank
     if (w && y.chunk) n += align256((size_t)y.units * rank * (N + K) * 4);
     return n;
 }
@@ -819,17 +1057,17 @@ extern "C" int32_t bakron_adapter_matmul(const void *X, int32_t type, int64_t ld
     uint32_t *p = c.take<uint32_t>(place_words(y));
     ShrinkArgs h = {};
     h.of = of, h.scale = scale, h.rank = rank, h.ranks = y.ranks, h.tiles = tiles;
-    h.job[0] = {static_cast<const char *>(X), static_cast<const char *>(A), ldx, K, rank * K, (int)K, p, nullptr};
+    h.job[0] = {static_cast<const char *>(X), static_cast<const char *>(A), ldx, rank * K, (int)K, 0, p, nullptr};
     ExpandArgs e = {};
-    e.of = of, e.tiles = tiles, e.p = p, e.w = static_cast<const char *>(B), e.group_w = N * rank, e.ldw = rank;
+    e.of = of, e.tiles = tiles, e.p = p, e.w = static_cast<const char *>(B), e.group_w = N * rank;
     e.base = static_cast<const char *>(base), e.out = static_cast<char *>(out), e.ldb = ldb, e.ldo = ldo;
-    e.N = (int)N, e.rank = rank, e.ranks = y.ranks;
+    e.N = (int)N, e.rank = rank, e.ranks = y.ranks, e.per_chunk = rank < 8 ? 0 : 65535 / (rank / 8) + 1;
     if (type == BAKRON_T_BF16) {
         launch_shrink<BAKRON_T_BF16>(h, y, 1, s);
-        launch_expand<BAKRON_T_BF16>(e, otype, y, s);
+        launch_expand<BAKRON_T_BF16, false>(e, otype, y, s);
     } else {
         launch_shrink<BAKRON_T_F16>(h, y, 1, s);
-        launch_expand<BAKRON_T_F16>(e, otype, y, s);
+        launch_expand<BAKRON_T_F16, false>(e, otype, y, s);
     }
     BK_LAUNCH_CHECK("adapter product");
     return BAKRON_OK;
@@ -838,7 +1076,7 @@ extern "C" int32_t bakron_adapter_matmul(const void *X, int32_t type, int64_t ld
 extern "C" size_t bakron_adapter_matmul_grad_workspace_size(int64_t rows, int64_t N, int64_t K, int32_t rank,
                                                             int32_t groups) {
     if (!sizes_ok(rows, N, K, rank, groups)) return 0;
-    return grad_size(layout_of(rows, N, K, rank, groups, true), N, K, rank, groups, true, true);
+    return grad_size(layout_of(rows, N, K, rank, groups, true), N, K, rank, true, true);
 }
 
 extern "C" int32_t bakron_adapter_matmul_grad(const void *dY, int64_t lddy, const void *X, int32_t type, int64_t ldx,
@@ -869,7 +1107,7 @@ extern "C" int32_t bakron_adapter_matmul_grad(const void *dY, int64_t lddy, cons
     BK_REQUIRE(aligned(dY, 2) && aligned(X, 2) && aligned(A, 2) && aligned(B, 2),
                "dY, X, A or B is misaligned for its type");
     const Layout y = layout_of(rows, N, K, rank, groups, true);
-    BK_TRY(check_ws(ws, ws_bytes, grad_size(y, N, K, rank, groups, dX, dA)));
+    BK_TRY(check_ws(ws, ws_bytes, grad_size(y, N, K, rank, dX, dA)));
     BK_TRY(check_device());
     hipStream_t s = static_cast<hipStream_t>(stream_);
     const Groups of = {offsets, order, groups, rows, dev_status};
@@ -877,33 +1115,18 @@ extern "C" int32_t bakron_adapter_matmul_grad(const void *dY, int64_t lddy, cons
     const char *a = static_cast<const char *>(A), *b = static_cast<const char *>(B);
     Carver c(ws);
     Tile *tiles = c.take<Tile>(y.slots);
-    char *bt = c.take<char>((size_t)groups * rank * N * 2), *at = nullptr;
-    uint32_t *u = nullptr, *ur = nullptr, *pr = nullptr;
-    if (dX) at = c.take<char>((size_t)groups * rank * K * 2), u = c.take<uint32_t>(place_words(y));
+    uint32_t *u = dX ? c.take<uint32_t>(place_words(y)) : nullptr, *ur = nullptr, *pr = nullptr;
     if (dA) ur = c.take<uint32_t>(place_words(y)), pr = c.take<uint32_t>(place_words(y));
     float *part = dA && y.chunk ? c.take<float>((size_t)y.units * rank * (N + K)) : nullptr;
 
-    TransposeArgs t = {};
-    t.of = of;
-    t.job[0] = {b, rank, N * rank, bt, (int)N, rank};
-    t.job[1] = {a, K, rank * K, at, rank, (int)K};
-    const int64_t blocks = ((std::max(N, dX ? K : 1) + 63) / 64) * ((rank + 63) / 64);
-    hipLaunchKernelGGL(transpose_kernel, dim3((unsigned)blocks, groups, dX ? 2 : 1), dim3(256), 0, s, t);
-
     ShrinkArgs h = {};
     h.of = of, h.scale = scale, h.rank = rank, h.ranks = y.ranks, h.tiles = tiles;
-    h.job[0] = {dy, bt, lddy, N, rank * N, (int)N, u, ur};
-    h.job[1] = {x, a, ldx, K, rank * K, (int)K, nullptr, pr};
+    h.job[0] = {dy, b, lddy, N * rank, (int)N, 1, u, ur};
+    h.job[1] = {x, a, ldx, rank * K, (int)K, 0, nullptr, pr};
     const int jobs = dA ? 2 : 1;
     type == BAKRON_T_BF16 ? launch_shrink<BAKRON_T_BF16>(h, y, jobs, s) : launch_shrink<BAKRON_T_F16>(h, y, jobs, s);
 
-    if (dX) {
-        ExpandArgs e = {};
-        e.of = of, e.tiles = tiles, e.p = u, e.w = at, e.group_w = K * rank, e.ldw = rank;
-        e.base = static_cast<const char *>(base), e.out = static_cast<char *>(dX), e.ldb = ldb, e.ldo = lddx;
-        e.N = (int)K, e.rank = rank, e.ranks = y.ranks;
-        type == BAKRON_T_BF16 ? launch_expand<BAKRON_T_BF16>(e, xtype, y, s) : launch_expand<BAKRON_T_F16>(e, xtype, y, s);
-    }
+    // X and dY are read again first, while caches may hold them
     if (dA) {
         OuterArgs o = {};
         o.of = of, o.rank = rank, o.ranks = y.ranks, o.high = 16 * y.mt, o.chunk = y.chunk, o.units = (int)y.units;
@@ -912,6 +1135,14 @@ extern "C" int32_t bakron_adapter_matmul_grad(const void *dY, int64_t lddy, cons
         o.job[0] = {x, ldx, (int)K, ur, static_cast<char *>(dA), K, rank * K, 0, 0};
         o.job[1] = {dy, lddy, (int)N, pr, static_cast<char *>(dB), rank, N * rank, 1, rank * K};
         type == BAKRON_T_BF16 ? launch_outer<BAKRON_T_BF16>(o, y, s) : launch_outer<BAKRON_T_F16>(o, y, s);
+    }
+    if (dX) {
+        ExpandArgs e = {};
+        e.of = of, e.tiles = tiles, e.p = u, e.w = a, e.group_w = K * rank;
+        e.base = static_cast<const char *>(base), e.out = static_cast<char *>(dX), e.ldb = ldb, e.ldo = lddx;
+        e.N = (int)K, e.rank = rank, e.ranks = y.ranks;
+        type == BAKRON_T_BF16 ? launch_expand<BAKRON_T_BF16, true>(e, xtype, y, s)
+                              : launch_expand<BAKRON_T_F16, true>(e, xtype, y, s);
     }
     BK_LAUNCH_CHECK("adapter gradients");
     return BAKRON_OK;

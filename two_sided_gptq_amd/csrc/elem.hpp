@@ -115,4 +115,16 @@ __device__ __forceinline__ void store8(char *base, int64_t i, int64_t left, cons
     }
 }
 
+// Sum of a lane's value and those of the lanes below it.  Rows of 16 lanes are
+// scanned first, then the rows' totals are passed on.
+__device__ __forceinline__ int wave_scan(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);   // from 1 lane below in the row
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, true);   // lane 15's to row 1, 47's to row 3
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, true);   // lane 31's to rows 2 and 3
+    return x;
+}
+
 }  // namespace bakron
