@@ -400,12 +400,6 @@ struct ExpandArgs {
     int per_chunk;          // 2^16 / (rank / 8), rounded up: divides what is below 2^11
 };
 
-// 8 elements as they are, of a 16-bit type or fp32.
-template <int T>
-struct Raw8 {
-    uint32_t w[T == BAKRON_T_F32 ? 8 : 4];
-};
-
 // D = W P^T with W's rows as the first operand: a lane then holds 4 of W's rows (columns of
 // out) for one place.  A workgroup takes a tile's places and 256 columns, a wave 64 of
 // them: W's part stays in registers, P in LDS.

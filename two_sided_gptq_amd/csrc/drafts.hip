@@ -92,13 +92,9 @@ __device__ __forceinline__ Row row_of(const DraftArgs &a, int64_t b, const Decis
     return r;
 }
 
-// Weights of tokens x .. x + 7; 0 from `left` on.
-template <int T>
-__device__ __forceinline__ void weights8(const Row &r, int x, int left, double *w) {
-    float p[8], q[8];
-    load8<T>(r.p, r.at_p + x, left, p);
+// Weights of tokens x .. x + 7 of p (and q where the row has one).
+__device__ __forceinline__ void weights_of(const Row &r, int x, const float *p, const float *q, double *w) {
     if (r.q) {
-        load8<T>(r.q, r.at_q + x, left, q);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const double d = (double)p[e] - (double)q[e];
@@ -109,6 +105,18 @@ __device__ __forceinline__ void weights8(const Row &r, int x, int left, double *
         for (int e = 0; e < 8; ++e) w[e] = p[e] < 0.0f || x + e == r.skip ? 0.0 : (double)p[e];
     }
 }
+// 0 from `left` on.
+template <int T>
+__device__ __forceinline__ void weights8(const Row &r, int x, int left, double *w) {
+    float p[8], q[8] = {};
+    load8<T>(r.p, r.at_p + x, left, p);
+    if (r.q) load8<T>(r.q, r.at_q + x, left, q);
+    weights_of(r, x, p, q, w);
+}
+
+__device__ __forceinline__ double sum8(const double *w) {
+    return ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+}
 
 __device__ __forceinline__ double wave_sum(double s) {
 #pragma unroll
@@ -116,16 +124,38 @@ __device__ __forceinline__ double wave_sum(double s) {
     return s;
 }
 
-// The wave's sum of the weights of tokens [lo, hi).
+// The wave's sum of the weights of tokens [lo, hi): steps of 512, the loads of 4 on their
+// way together.
 template <int T>
 __device__ __forceinline__ double stretch_sum(const Row &r, int lo, int hi) {
+    constexpr int U = 4, ES = Raw8<T>::ES;
     double s = 0.0;
-    const int lane = threadIdx.x & 63;
-#pragma unroll 4
-    for (int x = lo + lane * 8; x < hi; x += 512) {
+    const int lane = threadIdx.x & 63, steps = (hi - lo) / 512;
+    const char *p = r.p + (r.at_p + lo + lane * 8) * ES, *q = r.q ? r.q + (r.at_q + lo + lane * 8) * ES : nullptr;
+    for (int i = 0; i < steps; i += U) {
+        Raw8<T> rp[U], rq[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (i + k >= steps) break;
+            __builtin_memcpy(rp[k].w, p + (i + k) * 512 * ES, 8 * ES);
+            if (r.q) __builtin_memcpy(rq[k].w, q + (i + k) * 512 * ES, 8 * ES);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (i + k >= steps) break;
+            float x[8], y[8] = {};
+            double w[8];
+            unpack8<T>(rp[k].w, x);
+            if (r.q) unpack8<T>(rq[k].w, y);
+            weights_of(r, lo + (i + k) * 512 + lane * 8, x, y, w);
+            s += sum8(w);
+        }
+    }
+    const int x = lo + steps * 512 + lane * 8;
+    if (x < hi) {
         double w[8];
         weights8<T>(r, x, hi - x, w);
-        s += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+        s += sum8(w);
     }
     return wave_sum(s);
 }
@@ -250,10 +280,17 @@ __global__ __launch_bounds__(NT) void verify_kernel(DraftArgs a) {
     }
 }
 
-// Stretches that get a launch of their own, or 0: where few requests leave CUs idle.
+// Stretches that get a launch of their own, or 0.  A workgroup reads its two rows at about 1.2
+// us for 16384 tokens, as long as there are no more than CUs; a launch more costs about 2 us
+// and spreads that over the CUs that idle.  (One request: 32000 tokens 8.2 in two launches, 9.0
+// in one, 16384: 8.2 and 7.9; 128 requests of 131072 fp32: 28.3 and 32.7, of 50001: 16.9 and
+// 16.1.)  Stretches of 512 tokens at least, in about 1024 workgroups at most.
 int parts_of(int64_t batch, int64_t vocab) {
-    if (batch >= 64 || vocab < 16384) return 0;
-    return MAX_PARTS;
+    if (vocab * (256 - batch) < int64_t(6700000)) return 0;
+    int parts = MAX_PARTS;
+    while (parts > 8 && parts * batch > 4096) parts /= 2;
+    while (parts > 4 && (int64_t)parts * 512 > vocab) parts /= 2;
+    return parts;
 }
 
 template <int T>

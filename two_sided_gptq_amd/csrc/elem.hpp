@@ -60,6 +60,14 @@ __device__ __forceinline__ void unpack8(const uint32_t *w, float *x) {
     }
 }
 
+// 8 elements as they are in memory: loads that are not converted at once do not have to be
+// waited for before the next are asked for.
+template <int T>
+struct Raw8 {
+    static constexpr int ES = T == BAKRON_T_F32 ? 4 : 2;
+    uint32_t w[2 * ES];
+};
+
 // x[0..7] = elements i .. i + 7 of `base` as fp32; those from `left` on are 0
 // and not read.  The address needs the alignment of one element only.
 template <int T>

@@ -49,13 +49,14 @@ __device__ __forceinline__ void report(const SortArgs &a, bool bad) {
 
 // The lanes whose key is this lane's.
 __device__ __forceinline__ uint64_t peers_of(int key, int bits) {
-    uint64_t peers = ~uint64_t(0);
+    uint32_t lo = ~0u, hi = ~0u;
     for (int b = 0; b < bits; ++b) {
-        const bool s = (key >> b) & 1;
-        const uint64_t with = __ballot(s);
-        peers &= s ? with : ~with;
+        const int s = key << (31 - b) >> 31;  // all ones where the bit is set
+        const uint64_t with = __ballot(s < 0);
+        lo &= ~((uint32_t)with ^ s);
+        hi &= ~((uint32_t)(with >> 32) ^ s);
     }
-    return peers;
+    return (uint64_t)hi << 32 | lo;
 }
 
 // Adds the wave's 64 keys to count[] and returns how many equal keys the wave had met
@@ -73,16 +74,14 @@ __device__ __forceinline__ int rank_and_count(int *count, int key, int bits) {
 // Inclusive sum over the workgroup's threads (WAVES waves); part holds WAVES values.
 template <int WAVES>
 __device__ __forceinline__ int block_scan(int x, int *part) {
-    const int lane = lane_id(), w = threadIdx.x >> 6;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int y = __shfl_up(x, off);
-        if (lane >= off) x += y;
-    }
-    if (lane == 63) part[w] = x;
+    const int w = threadIdx.x >> 6;
+    x = wave_scan(x);
+    if (lane_id() == 63) part[w] = x;
     __syncthreads();
-    for (int v = 0; v < w; ++v) x += part[v];
-    return x;
+    int below = 0;
+#pragma unroll
+    for (int v = 0; v < WAVES - 1; ++v) below += v < w ? part[v] : 0;
+    return x + below;
 }
 
 // count[w][b] becomes the first slot of wave w's keys b: base (the pairs of the block
@@ -100,8 +99,9 @@ __device__ __forceinline__ void scan_bins(int bins, int *part, Total total, Star
     }
 }
 
-// Few pairs: one workgroup, one launch.  Each wave takes a contiguous stretch.
-constexpr int ONE_WAVES = 8, ONE_STEPS = 8, ONE_PAIRS = ONE_WAVES * ONE_STEPS * 64, ONE_GROUPS = 1024;
+// Few pairs: one workgroup, one launch.  Each wave takes a contiguous stretch.  A wave's ranks
+// are a chain of dependent steps, so many waves with few steps each are fastest.
+constexpr int ONE_WAVES = 16, ONE_STEPS = 4, ONE_PAIRS = ONE_WAVES * ONE_STEPS * 64, ONE_GROUPS = 1024;
 
 __global__ __launch_bounds__(64 * ONE_WAVES) void sort_one_kernel(SortArgs a) {
     __shared__ int count[ONE_WAVES][ONE_GROUPS + 2];
@@ -124,6 +124,7 @@ __global__ __launch_bounds__(64 * ONE_WAVES) void sort_one_kernel(SortArgs a) {
         bins, part,
         [&](int b) {
             int t = 0;
+#pragma unroll
             for (int v = 0; v < ONE_WAVES; ++v) t += count[v][b];
             return t;
         },
@@ -147,26 +148,29 @@ __global__ __launch_bounds__(64 * ONE_WAVES) void sort_one_kernel(SortArgs a) {
     }
 }
 
-// Many pairs: blocks of BLOCK_PAIRS count their bins; then each block adds up the counts of
-// the blocks before it and places its pairs.  From SCAN_BLOCKS blocks on the sums over
-// the blocks are a launch of their own.
-constexpr int BLOCK_WAVES = 4, BLOCK_STEPS = 16, BLOCK_PAIRS = BLOCK_WAVES * BLOCK_STEPS * 64, SCAN_BLOCKS = 64;
+// Many pairs: blocks of them count their bins; then each block adds up the counts of the
+// blocks before it and places its pairs.  From SCAN_BLOCKS blocks on the sums over the
+// blocks are a launch of their own.  A block has 8 waves with 4 steps each (65536 pairs, 128
+// groups: counting and placing 10.1 us, with 4 waves of 16 steps 16.2), beyond 2^20 pairs
+// with 16, which keeps the sums over the blocks short; more than 1024 groups leave LDS for the
+// counts of 4 waves only.
+constexpr int SCAN_BLOCKS = 64;
 
-__global__ __launch_bounds__(64 * BLOCK_WAVES) void sort_count_kernel(SortArgs a) {
+template <int WAVES, int STEPS>
+__global__ __launch_bounds__(64 * WAVES) void sort_count_kernel(SortArgs a) {
     __shared__ int count[MAX_GROUPS + 2];
     const int bins = a.groups + 1;
-    for (int b = threadIdx.x; b <= bins; b += 64 * BLOCK_WAVES) count[b] = 0;
-    int key[BLOCK_STEPS];
+    for (int b = threadIdx.x; b <= bins; b += 64 * WAVES) count[b] = 0;
+    int key[STEPS];
     bool bad = false;
 #pragma unroll
-    for (int s = 0; s < BLOCK_STEPS; ++s)
-        key[s] = bin_of(a, blockIdx.x * BLOCK_PAIRS + s * 64 * BLOCK_WAVES + threadIdx.x, bad);
+    for (int s = 0; s < STEPS; ++s) key[s] = bin_of(a, (blockIdx.x * STEPS + s) * 64 * WAVES + threadIdx.x, bad);
     report(a, bad);
     __syncthreads();
 #pragma unroll
-    for (int s = 0; s < BLOCK_STEPS; ++s) atomicAdd(count + key[s], 1);
+    for (int s = 0; s < STEPS; ++s) atomicAdd(count + key[s], 1);
     __syncthreads();
-    for (int b = threadIdx.x; b < bins; b += 64 * BLOCK_WAVES) a.hist[(int64_t)blockIdx.x * bins + b] = count[b];
+    for (int b = threadIdx.x; b < bins; b += 64 * WAVES) a.hist[(int64_t)blockIdx.x * bins + b] = count[b];
 }
 
 // A wave a bin.
@@ -178,42 +182,41 @@ __global__ __launch_bounds__(256) void sort_scan_kernel(SortArgs a) {
         const int k = k0 + lane;
         int32_t *at = a.hist + (int64_t)k * bins + b;
         const int c = k < a.blocks ? *at : 0;
-        int x = c;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const int y = __shfl_up(x, off);
-            if (lane >= off) x += y;
-        }
+        const int x = wave_scan(c);
         if (k < a.blocks) *at = sum + x - c;
-        sum += __shfl(x, 63);
+        sum += __builtin_amdgcn_readlane(x, 63);
     }
     if (lane == 0) a.total[b] = sum;
 }
 
-template <bool SCANNED>
-__global__ __launch_bounds__(64 * BLOCK_WAVES) void sort_place_kernel(SortArgs a) {
+template <int WAVES, int STEPS, bool SCANNED>
+__global__ __launch_bounds__(64 * WAVES) void sort_place_kernel(SortArgs a) {
     extern __shared__ int space[];
     const int lane = lane_id(), w = threadIdx.x >> 6, bins = a.groups + 1;
-    int *count = space;                                // [BLOCK_WAVES][bins + 1]
-    int *total = space + BLOCK_WAVES * (bins + 1);     // [bins]
+    int *count = space;                                // [WAVES][bins + 1]
+    int *total = space + WAVES * (bins + 1);     // [bins]
     int *before = total + bins;                        // [bins]: of this block's bins, in earlier blocks
     int *part = before + bins;
-    int key[BLOCK_STEPS], rank[BLOCK_STEPS];
+    int key[STEPS], rank[STEPS];
     bool bad = false;
-    const int i0 = blockIdx.x * BLOCK_PAIRS + w * BLOCK_STEPS * 64 + lane;
+    const int i0 = blockIdx.x * (64 * WAVES * STEPS) + w * STEPS * 64 + lane;
 #pragma unroll
-    for (int s = 0; s < BLOCK_STEPS; ++s) key[s] = bin_of(a, i0 + s * 64, bad);
-    for (int b = threadIdx.x; b < bins; b += 64 * BLOCK_WAVES) {
+    for (int s = 0; s < STEPS; ++s) key[s] = bin_of(a, i0 + s * 64, bad);
+    for (int b = threadIdx.x; b < bins; b += 64 * WAVES) {
         if constexpr (SCANNED) {
             total[b] = a.total[b];
             before[b] = a.hist[(int64_t)blockIdx.x * bins + b];
         } else {
             int t = 0, f = 0;
-#pragma unroll 16
-            for (int k = 0; k < a.blocks; ++k) {
-                const int c = a.hist[(int64_t)k * bins + b];
-                t += c;
-                f += k < (int)blockIdx.x ? c : 0;
+            for (int k0 = 0; k0 < a.blocks; k0 += 32) {
+                int c[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) c[k] = k0 + k < a.blocks ? a.hist[(int64_t)(k0 + k) * bins + b] : 0;
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    t += c[k];
+                    f += k0 + k < (int)blockIdx.x ? c[k] : 0;
+                }
             }
             total[b] = t;
             before[b] = f;
@@ -223,14 +226,14 @@ __global__ __launch_bounds__(64 * BLOCK_WAVES) void sort_place_kernel(SortArgs a
     for (int b = lane; b <= bins; b += 64) mine[b] = 0;
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int s = 0; s < BLOCK_STEPS; ++s) rank[s] = rank_and_count(mine, key[s], a.bits);
+    for (int s = 0; s < STEPS; ++s) rank[s] = rank_and_count(mine, key[s], a.bits);
     __syncthreads();
-    scan_bins<BLOCK_WAVES>(
+    scan_bins<WAVES>(
         bins, part, [&](int b) { return total[b]; },
         [&](int b, int at) {
             if (blockIdx.x == 0) a.offsets[b] = at;
             at += before[b];
-            for (int v = 0; v < BLOCK_WAVES; ++v) {
+            for (int v = 0; v < WAVES; ++v) {
                 const int c = count[v * (bins + 1) + b];
                 count[v * (bins + 1) + b] = at;
                 at += c;
@@ -238,7 +241,7 @@ __global__ __launch_bounds__(64 * BLOCK_WAVES) void sort_place_kernel(SortArgs a
         });
     __syncthreads();
 #pragma unroll
-    for (int s = 0; s < BLOCK_STEPS; ++s) {
+    for (int s = 0; s < STEPS; ++s) {
         const int i = i0 + s * 64;
         if (i < a.n) {
             const int slot = mine[key[s]] + rank[s];
@@ -249,7 +252,29 @@ __global__ __launch_bounds__(64 * BLOCK_WAVES) void sort_place_kernel(SortArgs a
 }
 
 bool sort_in_one(int64_t n, int groups) { return n <= ONE_PAIRS && groups <= ONE_GROUPS; }
-int64_t sort_blocks(int64_t n) { return (n + BLOCK_PAIRS - 1) / BLOCK_PAIRS; }
+struct SortShape {
+    int waves, steps;
+    int64_t blocks;
+};
+SortShape sort_shape(int64_t n, int groups) {
+    SortShape y = {groups > ONE_GROUPS ? 4 : 8, 16, 0};
+    if (y.waves == 8 && n <= 1 << 20) y.steps = 4;
+    y.blocks = (n + 64 * y.waves * y.steps - 1) / (64 * y.waves * y.steps);
+    return y;
+}
+
+template <int WAVES, int STEPS>
+void launch_sort(const SortArgs &a, hipStream_t s) {
+    const dim3 grid(a.blocks), block(64 * WAVES);
+    const size_t lds = (WAVES * (a.groups + 2) + 2 * (a.groups + 1) + WAVES) * sizeof(int);
+    hipLaunchKernelGGL((sort_count_kernel<WAVES, STEPS>), grid, block, 0, s, a);
+    if (a.blocks > SCAN_BLOCKS) {
+        hipLaunchKernelGGL(sort_scan_kernel, dim3((a.groups + 1 + 3) / 4), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((sort_place_kernel<WAVES, STEPS, true>), grid, block, lds, s, a);
+    } else {
+        hipLaunchKernelGGL((sort_place_kernel<WAVES, STEPS, false>), grid, block, lds, s, a);
+    }
+}
 
 // ---------------------------------------------------------------- rows
 
@@ -264,6 +289,7 @@ struct RowsArgs {
     int64_t token0;        // the launch's first
     int tokens, k, cols, segs;
     int64_t n;             // pairs
+    int past_caches;       // fp8, gradient: rows of the output are in whole pieces of a lane, and many
     int32_t *dev_status;
 };
 
@@ -307,13 +333,6 @@ __device__ __forceinline__ int from_lane(int x, int lane) { return __builtin_amd
 __device__ __forceinline__ float from_lane(float x, int lane) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
 }
-
-// 8 elements as they are.
-template <int T>
-struct Raw8 {
-    static constexpr int ES = T == BAKRON_T_F32 ? 4 : 2;
-    uint32_t w[2 * ES];
-};
 
 // Raw elements i .. i + 7; those from `left` on are 0 and not read.
 template <int T>
@@ -375,6 +394,14 @@ __global__ __launch_bounds__(256) void gather_kernel(RowsArgs a) {
     }
 }
 
+// Codes past the caches, whole 8 bytes only: 65536 rows of 4096 go in 64 instead of 84 us, as
+// the lines that the scattered scales fill, 4 bytes at a time, then stay in L2 until they
+// are whole.  (Past the caches too, the scales alone take 70 us more.)
+__device__ __forceinline__ void store_past(uint8_t *to, uint2 c) {
+    typedef uint32_t uintx2 __attribute__((ext_vector_type(2)));
+    __builtin_nontemporal_store(uintx2{c.x, c.y}, reinterpret_cast<uintx2 *>(to));
+}
+
 // Copies in fp8: 16 lanes hold a block of 128 columns, so its maximum stays inside a
 // DPP row; each block is rounded once for all its copies.  A dropped row gets codes 0 and
 // scales 1, as a row of zeros would.
@@ -406,6 +433,7 @@ __global__ __launch_bounds__(256) void gather_fp8_kernel(RowsArgs a) {
         code[s] = encode8(x[s], inv, bad);
     }
     bool used = false;
+    const bool past = a.past_caches;
     uint8_t *out = reinterpret_cast<uint8_t *>(a.out);
     for (int j = 0; j < a.k; ++j) {
         const int slot = from_lane(slots, j);
@@ -415,7 +443,12 @@ __global__ __launch_bounds__(256) void gather_fp8_kernel(RowsArgs a) {
 #pragma unroll
         for (int s = 0; s < PARTS; ++s)
             if (col[s] < a.cols) {
-                store8(out + slot * a.ldo + col[s], kept ? code[s] : make_uint2(0, 0), min(8, a.cols - col[s]));
+                uint8_t *to = out + slot * a.ldo + col[s];
+                const uint2 c = kept ? code[s] : make_uint2(0, 0);
+                if (past && col[s] + 8 <= a.cols)
+                    store_past(to, c);
+                else
+                    store8(to, c, min(8, a.cols - col[s]));
                 if ((lane_id() & 15) == 0) a.scales[(int64_t)(col[s] >> 7) * a.n + slot] = kept ? scale[s] : 1.0f;
             }
     }
@@ -456,6 +489,24 @@ __global__ __launch_bounds__(256) void combine_kernel(RowsArgs a) {
     store8<T>(a.out, p.token * a.ldo + col, left, sum);
 }
 
+// 8 values past the caches, to whole 16 bytes (16384 rows of 4096 bf16: 61 against 64 us).
+template <int T>
+__device__ __forceinline__ void store8_past(char *base, int64_t i, const float *x) {
+    typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
+    if constexpr (T == BAKRON_T_F32) {
+        uintx4 *to = reinterpret_cast<uintx4 *>(base + 4 * i);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            __builtin_nontemporal_store(uintx4{__float_as_uint(x[4 * h]), __float_as_uint(x[4 * h + 1]),
+                                               __float_as_uint(x[4 * h + 2]), __float_as_uint(x[4 * h + 3])},
+                                        to + h);
+    } else {
+        __builtin_nontemporal_store(uintx4{pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]),
+                                           pack2<T>(x[6], x[7])},
+                                    reinterpret_cast<uintx4 *>(base + 2 * i));
+    }
+}
+
 // dY[slot] = w dout[t];  dw[t][j] = <dout[t], Y[slot]>, summed over a lane's columns, the
 // lanes and the waves in a fixed order.  WAVES waves take a token.
 template <int T, int WAVES>
@@ -467,6 +518,7 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(RowsArgs a) {
     const int64_t token = a.token0 + (mine ? at : 0);
     const int end = rows_in_groups(a), slots = slots_of(a, token);
     const float weights = weights_of(a, token);
+    const bool past = a.past_caches;
     for (int j0 = 0; j0 < a.k; j0 += BATCH) {
         float dot[BATCH] = {}, weight[BATCH];
         int slot[BATCH];  // -1: none
@@ -496,7 +548,10 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(RowsArgs a) {
                         dy[q] = weight[j] * d[q];
                     }
                 }
-                store8<T>(a.out, slot[j] * a.ldo + col, left, dy);
+                if (past && left >= 8)
+                    store8_past<T>(a.out, slot[j] * a.ldo + col, dy);
+                else
+                    store8<T>(a.out, slot[j] * a.ldo + col, left, dy);
             }
         }
 #pragma unroll
@@ -551,7 +606,7 @@ void launch_gather(const RowsArgs &a, int64_t tokens, bool fp8, hipStream_t s) {
     if (a.cols <= 512 || tokens <= 512)
         launch_gather<T, 1>(a, tokens, fp8, s);
     else
-        launch_gather<T, 4>(a, tokens, fp8, s);
+        launch_gather<T, 2>(a, tokens, fp8, s);
 }
 
 template <int T>
@@ -583,6 +638,9 @@ void by_type(int32_t type, F f) {
 
 bool aligned(const void *p, int64_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
+// With fewer bytes than the L2s hold, whoever comes next finds them there.
+bool many(int64_t bytes) { return bytes > int64_t(32) << 20; }
+
 int32_t check_rows(int32_t type, int64_t tokens, int32_t k, int64_t cols, int32_t groups) {
     BK_REQUIRE(type == BAKRON_T_F32 || type == BAKRON_T_BF16 || type == BAKRON_T_F16, "bad type %d", type);
     BK_REQUIRE(tokens >= 1 && k >= 1 && k <= MAX_CHOICES && tokens <= MAX_PAIRS / k && cols >= 1 && cols <= MAX_PAIRS,
@@ -610,7 +668,7 @@ using namespace bakron;
 
 extern "C" size_t bakron_group_sort_workspace_size(int64_t n, int32_t groups) {
     if (n < 1 || n > MAX_PAIRS || groups < 1 || groups > MAX_GROUPS || sort_in_one(n, groups)) return 0;
-    return align256(sort_blocks(n) * (groups + 1) * sizeof(int32_t)) + align256((groups + 1) * sizeof(int32_t));
+    return align256(sort_shape(n, groups).blocks * (groups + 1) * sizeof(int32_t)) + align256((groups + 1) * sizeof(int32_t));
 }
 
 extern "C" int32_t bakron_group_sort(const void *ids, int32_t id_bits, int64_t n, int32_t groups, int32_t *offsets,
@@ -638,19 +696,17 @@ extern "C" int32_t bakron_group_sort(const void *ids, int32_t id_bits, int64_t n
         BK_LAUNCH_CHECK("sort_one_kernel");
         return BAKRON_OK;
     }
-    a.blocks = (int)sort_blocks(n);
+    const SortShape y = sort_shape(n, groups);
+    a.blocks = (int)y.blocks;
     Carver c(ws);
     a.hist = c.take<int32_t>((size_t)a.blocks * (groups + 1));
     a.total = c.take<int32_t>(groups + 1);
-    const dim3 grid(a.blocks), block(64 * BLOCK_WAVES);
-    const size_t lds = (BLOCK_WAVES * (groups + 2) + 2 * (groups + 1) + BLOCK_WAVES) * sizeof(int);
-    hipLaunchKernelGGL(sort_count_kernel, grid, block, 0, s, a);
-    if (a.blocks > SCAN_BLOCKS) {
-        hipLaunchKernelGGL(sort_scan_kernel, dim3((groups + 1 + 3) / 4), dim3(256), 0, s, a);
-        hipLaunchKernelGGL(sort_place_kernel<true>, grid, block, lds, s, a);
-    } else {
-        hipLaunchKernelGGL(sort_place_kernel<false>, grid, block, lds, s, a);
-    }
+    if (y.waves == 4)
+        launch_sort<4, 16>(a, s);
+    else if (y.steps == 4)
+        launch_sort<8, 4>(a, s);
+    else
+        launch_sort<8, 16>(a, s);
     BK_LAUNCH_CHECK("group sort");
     return BAKRON_OK;
 }
@@ -686,6 +742,7 @@ extern "C" int32_t bakron_group_gather_fp8(const void *X, int32_t type, int64_t 
     RowsArgs a = {};
     a.x = static_cast<const char *>(X), a.out = reinterpret_cast<char *>(Q), a.ldx = ldx, a.ldo = ldq;
     a.slots = slots, a.end = offsets + groups, a.k = k, a.cols = (int)cols, a.n = tokens * k, a.scales = scales;
+    a.past_caches = many(a.n * cols) && ldq % 8 == 0 && aligned(Q, 8);
     a.dev_status = dev_status;
     by_type(type, [&](auto t) { launch_gather<t.value>(a, tokens, true, static_cast<hipStream_t>(stream_)); });
     BK_LAUNCH_CHECK("gather_fp8_kernel");
@@ -730,6 +787,7 @@ extern "C" int32_t bakron_group_combine_grad(const void *dout, int64_t ldd, cons
     a.x = static_cast<const char *>(Y), a.dout = static_cast<const char *>(dout), a.out = static_cast<char *>(dY);
     a.ldx = ldy, a.ldd = ldd, a.ldo = lddy, a.slots = slots, a.end = offsets + groups, a.weights = weights;
     a.dweights = dweights, a.k = k, a.cols = (int)cols, a.n = tokens * k, a.dev_status = dev_status;
+    a.past_caches = many(a.n * cols * elem_size(type)) && lddy * elem_size(type) % 16 == 0 && aligned(dY, 16);
     by_type(type, [&](auto t) { launch_combine<t.value>(a, tokens, static_cast<hipStream_t>(stream_)); });
     BK_LAUNCH_CHECK("combine_grad_kernel");
     return BAKRON_OK;
