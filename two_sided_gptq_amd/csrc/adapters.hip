@@ -186,7 +186,10 @@ struct ShrinkArgs {
     const float *scale;     // of a group, or NULL
     int rank, ranks;        // ranks: in whole 16s
     int high, slots;        // places of a tile, tiles
-    Tile *tiles;            // written by the first job
+    int splits;             // workgroups that share K, without GRAD: sums are then left in parts
+    int64_t part_words;     // of a part
+    Tile *tiles;            // written by the first job, as are
+    int32_t *rows;          // the rows of the tiles' places
 };
 
 // The least tile is for few rows: its workgroup streams K with as many waves as fit.
@@ -210,10 +213,12 @@ __global__ __launch_bounds__(64 * shrink_waves(MT, RT), GRAD && MT * RT == 8 ? 2
     const int block = blockIdx.x, sub = (block >> 3) % parts * MT;
     int slot = (block >> 3) / parts * 8 + (block & 7);
     if (slot >= a.slots) return;
-    const Shrink &job = a.job[blockIdx.z];
+    const Shrink &job = a.job[GRAD ? blockIdx.z : 0];
+    const int part = GRAD ? 0 : blockIdx.z, splits = GRAD ? 1 : a.splits;
     Tile t = tile_of(a.of, a.high, slot, a.slots);
     if (blockIdx.y == 0 && blockIdx.z == 0 && sub == 0) {
         if (threadIdx.x == 0) a.tiles[slot] = t;
+        if ((int)threadIdx.x < a.high) a.rows[slot * a.high + threadIdx.x] = row_at(a.of, t.p0 + threadIdx.x, t.p1);
         report(a.of, t, block == 0);
     }
     t.p0 += sub * 16;
@@ -264,13 +269,14 @@ __global__ __launch_bounds__(64 * shrink_waves(MT, RT), GRAD && MT * RT == 8 ? 2
     // KS of K a step, DEPTH steps on their way.  Workgroups begin at different columns: rows of
     // a power of two in bytes would otherwise have all of them at the same memory channels.
     const int whole = job.K / KS, turned = whole ? (int)((int64_t)blockIdx.x * waves % whole) : 0;
+    const int all = waves * splits, first = part * waves + w;  // waves that share K
     auto step = [&](int s) { return s + turned < whole ? s + turned : s + turned - whole; };
     uintx4 vx[DEPTH][MT][NL], vm[DEPTH][RT][NL];
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d)
-        if (w + d * waves < whole)
+        if (first + d * all < whole)
 #pragma unroll
-            for (int j = 0; j < RT; ++j) load_w(step(w + d * waves), j, vm[d][j]);
+            for (int j = 0; j < RT; ++j) load_w(step(first + d * all), j, vm[d][j]);
     int row[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
@@ -333,15 +339,15 @@ __global__ __launch_bounds__(64 * shrink_waves(MT, RT), GRAD && MT * RT == 8 ? 2
     };
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d)
-        if (w + d * waves < whole)
+        if (first + d * all < whole)
 #pragma unroll
-            for (int i = 0; i < MT; ++i) load_x(step(w + d * waves), i, vx[d][i]);
-    for (int s = w; s < whole; s += DEPTH * waves) {
+            for (int i = 0; i < MT; ++i) load_x(step(first + d * all), i, vx[d][i]);
+    for (int s = first; s < whole; s += DEPTH * all) {
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d)
-            if (s + d * waves < whole) multiply(vx[d], vm[d], s + (d + DEPTH) * waves);
+            if (s + d * all < whole) multiply(vx[d], vm[d], s + (d + DEPTH) * all);
     }
-    if (whole * KS < job.K && w == whole % waves) {
+    if (whole * KS < job.K && first == whole % all) {
         const int k = whole * KS, left = job.K - k - lc * 8;
 #pragma unroll
         for (int h = 0; h < NL; ++h) {
@@ -376,12 +382,13 @@ __global__ __launch_bounds__(64 * shrink_waves(MT, RT), GRAD && MT * RT == 8 ? 2
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const bool ok = __shfl(row[i], q * 4 + e) >= 0 && rank < a.rank;
-                packed[e] = ok ? pack_parts(s[e] * scale) : 0;
+                const float x = ok ? s[e] * scale : 0.0f;
+                packed[e] = splits > 1 ? __float_as_uint(x) : pack_parts(x);
             }
             if (job.by_rank) *reinterpret_cast<uintx4 *>(job.by_rank + (tile * a.ranks + rank) * 16 + q * 4) = packed;
             if (job.by_place)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) job.by_place[(tile * 16 + q * 4 + e) * a.ranks + rank] = packed[e];
+                for (int e = 0; e < 4; ++e) job.by_place[part * a.part_words + (tile * 16 + q * 4 + e) * a.ranks + rank] = packed[e];
         }
 }
 
@@ -390,7 +397,10 @@ __global__ __launch_bounds__(64 * shrink_waves(MT, RT), GRAD && MT * RT == 8 ? 2
 struct ExpandArgs {
     Groups of;
     const Tile *tiles;
-    const uint32_t *p;      // [16-place tile][16][ranks]
+    const int32_t *rows;    // of the tiles' places
+    const uint32_t *p;      // [16-place tile][16][ranks]; with splits > 1 so many parts of sums in fp32
+    int splits;
+    int64_t part_words;
     const char *w;          // a group's matrix
     int64_t group_w;        // STRIDED: rank x N, else N x rank
     const char *base;       // may be out; NULL: 0
@@ -426,7 +436,14 @@ __device__ __forceinline__ void stage_p(const ExpandArgs &a, int64_t sub, int co
     const int words = (count + 15) / 16 * 16 * a.ranks;
     for (int i = threadIdx.x * 4; i < words; i += 1024) {
         const int r = i / a.ranks, c = i - r * a.ranks;
-        *reinterpret_cast<uintx4 *>(lds + r * (a.ranks + 4) + c) = *reinterpret_cast<const uintx4 *>(p + i);
+        uintx4 v = *reinterpret_cast<const uintx4 *>(p + i);
+        if (a.splits > 1) {
+            floatx4 sum = __builtin_bit_cast(floatx4, v);
+            for (int k = 1; k < a.splits; ++k) sum += *reinterpret_cast<const floatx4 *>(p + k * a.part_words + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = pack_parts(sum[e]);
+        }
+        *reinterpret_cast<uintx4 *>(lds + r * (a.ranks + 4) + c) = v;
     }
 }
 
@@ -450,7 +467,10 @@ __device__ __forceinline__ void expand_whole(const ExpandArgs &a, const Tile &t,
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) row[i][h] = row_at(a.of, t.p0 + i * 16 + h * 8 + lr, t.p1);
+        for (int h = 0; h < 2; ++h) {
+            const int place = i * 16 + h * 8 + lr, r = a.rows[slot * (16 * MT) + place];
+            row[i][h] = place < count ? r : -1;
+        }
     const int chunks = a.rank / 8, some = 16 * PER * chunks;  // 16-byte pieces of a row, of a pass
     const char *wg = a.w + 2 * ((none ? 0 : t.g) * a.group_w);
     uintx4 raw_w[4 * RS];
@@ -590,7 +610,7 @@ __device__ __forceinline__ void expand_any(const ExpandArgs &a, const Tile &t, i
     if (!none) stage_p(a, slot * MT, count, lds);
     __syncthreads();
     for (int i = 0; i * 16 < count; ++i) {
-        const int row = row_at(a.of, t.p0 + i * 16 + l, t.p1);
+        const int row = i * 16 + l < count ? a.rows[slot * (16 * MT) + i * 16 + l] : -1;
         float y[2][8] = {};
         if (a.base && row >= 0)
 #pragma unroll
@@ -866,6 +886,7 @@ struct Layout {
     int rt;                 // 16-rank blocks of a workgroup of shrink
     int ranks, rs;          // ranks in whole 16s; 32-rank steps of expand
     int64_t slots;          // tiles of 16 mt places
+    int splits;             // of K, in shrink
     int chunk;              // of the sums over places; 0: a group is one unit
     int64_t units;
 };
@@ -881,14 +902,21 @@ Layout layout_of(int64_t rows, int64_t N, int64_t K, int32_t rank, int32_t group
     y.slots = row_tiles(16 * y.mt, rows, groups, true);
     const int blocks = y.ranks / 16;
     y.rt = y.mt == 1 && y.slots * blocks <= 1024 ? 1 : blocks >= 4 ? 4 : blocks >= 2 ? 2 : 1;
+    // Where CUs idle, several workgroups share a tile's K, 2 steps a wave at least (8 rows of
+    // their own adapters, rank 16, K = 14336: 10.3 us, unshared 14.9; 64 rows, K = 4096: 10.9 and
+    // 11.9).
+    y.splits = 1;
+    if (!grad && y.mt == 1 && y.rt == 1)
+        while (y.splits < 8 && y.slots * blocks * y.splits * 2 <= 256 && K >= (int64_t)SHRINK_STEP * 16 * 2 * y.splits * 2) y.splits *= 2;
     y.chunk = 0;
     y.units = groups;
+    // Sums over places: a group at a time, or, where that leaves CUs idle and there are places
+    // enough to pay for joining, chunks of a group.
     if (grad) {
         const int64_t tiles = (N + 127) / 128 + (K + 127) / 128, want = 512;
-        if (tiles * groups < want && rows > 512) {
+        if (tiles * groups < want && rows > 2048) {
             const int64_t splits = (want + tiles - 1) / tiles;
-            y.chunk = (int)round_up((rows + splits - 1) / splits, 128);
-            if (y.chunk < 512) y.chunk = 512;
+            y.chunk = (int)std::max<int64_t>(512, round_up((rows + splits - 1) / splits, 128));
             y.units = row_tiles(y.chunk, rows, groups, true);
         }
     }
@@ -898,24 +926,24 @@ Layout layout_of(int64_t rows, int64_t N, int64_t K, int32_t rank, int32_t group
 size_t place_words(const Layout &y) { return (size_t)y.slots * y.mt * 16 * y.ranks; }
 
 template <int T, int MT, int RT>
-void launch_shrink(const ShrinkArgs &a, const Layout &y, int jobs, hipStream_t s) {
-    const dim3 grid((unsigned)(round_up(y.slots, 8) * (y.mt / MT)), (unsigned)((y.ranks / 16 + RT - 1) / RT), jobs);
+void launch_shrink(const ShrinkArgs &a, const Layout &y, int deep, hipStream_t s) {
+    const dim3 grid((unsigned)(round_up(y.slots, 8) * (y.mt / MT)), (unsigned)((y.ranks / 16 + RT - 1) / RT), deep);
     if (a.job[0].strided)
         hipLaunchKernelGGL((shrink_kernel<T, MT, RT, true>), grid, dim3(64 * shrink_waves(MT, RT)), shrink_lds(MT, RT), s, a);
     else
         hipLaunchKernelGGL((shrink_kernel<T, MT, RT, false>), grid, dim3(64 * shrink_waves(MT, RT)), shrink_lds(MT, RT), s, a);
 }
 template <int T>
-void launch_shrink(ShrinkArgs a, const Layout &y, int jobs, hipStream_t s) {
-    a.high = 16 * y.mt, a.slots = (int)y.slots;
+void launch_shrink(ShrinkArgs a, const Layout &y, int deep, hipStream_t s) {
+    a.high = 16 * y.mt, a.slots = (int)y.slots, a.splits = y.splits, a.part_words = place_words(y);
     if (shrink_mt(y) == 1) {
-        if (y.rt == 1) return launch_shrink<T, 1, 1>(a, y, jobs, s);
-        if (y.rt == 2) return launch_shrink<T, 1, 2>(a, y, jobs, s);
-        return launch_shrink<T, 1, 4>(a, y, jobs, s);
+        if (y.rt == 1) return launch_shrink<T, 1, 1>(a, y, deep, s);
+        if (y.rt == 2) return launch_shrink<T, 1, 2>(a, y, deep, s);
+        return launch_shrink<T, 1, 4>(a, y, deep, s);
     }
-    if (y.rt == 1) return launch_shrink<T, 2, 1>(a, y, jobs, s);
-    if (y.rt == 2) return launch_shrink<T, 2, 2>(a, y, jobs, s);
-    launch_shrink<T, 2, 4>(a, y, jobs, s);
+    if (y.rt == 1) return launch_shrink<T, 2, 1>(a, y, deep, s);
+    if (y.rt == 2) return launch_shrink<T, 2, 2>(a, y, deep, s);
+    launch_shrink<T, 2, 4>(a, y, deep, s);
 }
 
 template <int T, int OT, int MT, bool STRIDED>
@@ -1000,8 +1028,10 @@ int32_t check_ws(const void *ws, size_t have, size_t need) {
     return BAKRON_ERR_WORKSPACE;
 }
 
+size_t tiles_size(const Layout &y) { return align256(y.slots * sizeof(Tile)) + align256(y.slots * 16 * y.mt * sizeof(int32_t)); }
+
 size_t grad_size(const Layout &y, int64_t N, int64_t K, int32_t rank, bool x, bool w) {
-    size_t n = align256(y.slots * sizeof(Tile));
+    size_t n = tiles_size(y);
     if (x) n += align256(place_words(y) * 4);      // U by place
     if (w) n += 2 * align256(place_words(y) * 4);  // U and P by rank
     if (w && y.chunk) n += align256((size_t)y.units * rank * (N + K) * 4);
@@ -1023,7 +1053,7 @@ extern "C" size_t bakron_adapter_matmul_workspace_size(int64_t rows, int64_t N, 
                                                        int32_t groups) {
     if (!sizes_ok(rows, N, K, rank, groups)) return 0;
     const Layout y = layout_of(rows, N, K, rank, groups, false);
-    return align256(y.slots * sizeof(Tile)) + align256(place_words(y) * 4);
+    return tiles_size(y) + align256(y.splits * place_words(y) * 4);
 }
 
 extern "C" int32_t bakron_adapter_matmul(const void *X, int32_t type, int64_t ldx, const void *A, const void *B,
@@ -1048,19 +1078,20 @@ extern "C" int32_t bakron_adapter_matmul(const void *X, int32_t type, int64_t ld
     const Groups of = {offsets, order, groups, rows, dev_status};
     Carver c(ws);
     Tile *tiles = c.take<Tile>(y.slots);
-    uint32_t *p = c.take<uint32_t>(place_words(y));
+    int32_t *place_rows = c.take<int32_t>(y.slots * 16 * y.mt);
+    uint32_t *p = c.take<uint32_t>(y.splits * place_words(y));
     ShrinkArgs h = {};
-    h.of = of, h.scale = scale, h.rank = rank, h.ranks = y.ranks, h.tiles = tiles;
+    h.of = of, h.scale = scale, h.rank = rank, h.ranks = y.ranks, h.tiles = tiles, h.rows = place_rows;
     h.job[0] = {static_cast<const char *>(X), static_cast<const char *>(A), ldx, rank * K, (int)K, 0, p, nullptr};
     ExpandArgs e = {};
-    e.of = of, e.tiles = tiles, e.p = p, e.w = static_cast<const char *>(B), e.group_w = N * rank;
+    e.of = of, e.tiles = tiles, e.rows = place_rows, e.splits = y.splits, e.part_words = place_words(y), e.p = p, e.w = static_cast<const char *>(B), e.group_w = N * rank;
     e.base = static_cast<const char *>(base), e.out = static_cast<char *>(out), e.ldb = ldb, e.ldo = ldo;
     e.N = (int)N, e.rank = rank, e.ranks = y.ranks, e.per_chunk = rank < 8 ? 0 : 65535 / (rank / 8) + 1;
     if (type == BAKRON_T_BF16) {
-        launch_shrink<BAKRON_T_BF16>(h, y, 1, s);
+        launch_shrink<BAKRON_T_BF16>(h, y, y.splits, s);
         launch_expand<BAKRON_T_BF16, false>(e, otype, y, s);
     } else {
-        launch_shrink<BAKRON_T_F16>(h, y, 1, s);
+        launch_shrink<BAKRON_T_F16>(h, y, y.splits, s);
         launch_expand<BAKRON_T_F16, false>(e, otype, y, s);
     }
     BK_LAUNCH_CHECK("adapter product");
@@ -1109,12 +1140,13 @@ extern "C" int32_t bakron_adapter_matmul_grad(const void *dY, int64_t lddy, cons
     const char *a = static_cast<const char *>(A), *b = static_cast<const char *>(B);
     Carver c(ws);
     Tile *tiles = c.take<Tile>(y.slots);
+    int32_t *place_rows = c.take<int32_t>(y.slots * 16 * y.mt);
     uint32_t *u = dX ? c.take<uint32_t>(place_words(y)) : nullptr, *ur = nullptr, *pr = nullptr;
     if (dA) ur = c.take<uint32_t>(place_words(y)), pr = c.take<uint32_t>(place_words(y));
     float *part = dA && y.chunk ? c.take<float>((size_t)y.units * rank * (N + K)) : nullptr;
 
     ShrinkArgs h = {};
-    h.of = of, h.scale = scale, h.rank = rank, h.ranks = y.ranks, h.tiles = tiles;
+    h.of = of, h.scale = scale, h.rank = rank, h.ranks = y.ranks, h.tiles = tiles, h.rows = place_rows;
     h.job[0] = {dy, b, lddy, N * rank, (int)N, 1, u, ur};
     h.job[1] = {x, a, ldx, rank * K, (int)K, 0, nullptr, pr};
     const int jobs = dA ? 2 : 1;
@@ -1132,7 +1164,7 @@ extern "C" int32_t bakron_adapter_matmul_grad(const void *dY, int64_t lddy, cons
     }
     if (dX) {
         ExpandArgs e = {};
-        e.of = of, e.tiles = tiles, e.p = u, e.w = a, e.group_w = K * rank;
+        e.of = of, e.tiles = tiles, e.rows = place_rows, e.splits = 1, e.p = u, e.w = a, e.group_w = K * rank;
         e.base = static_cast<const char *>(base), e.out = static_cast<char *>(dX), e.ldb = ldb, e.ldo = lddx;
         e.N = (int)K, e.rank = rank, e.ranks = y.ranks;
         type == BAKRON_T_BF16 ? launch_expand<BAKRON_T_BF16, true>(e, xtype, y, s)

@@ -289,7 +289,7 @@ struct RowsArgs {
     int64_t token0;        // the launch's first
     int tokens, k, cols, segs;
     int64_t n;             // pairs
-    int past_caches;       // fp8, gradient: rows of the output are in whole pieces of a lane, and many
+    int past_caches;       // the output goes past the caches
     int32_t *dev_status;
 };
 
@@ -334,6 +334,18 @@ __device__ __forceinline__ float from_lane(float x, int lane) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
 }
 
+// PIECES x 16 bytes past the caches.  What is written once and is more than the L2s hold
+// would only push out what is read: copies of 4096 rows to 16384 of 2048 fp16 in 20.3
+// instead of 28.9 us, with rows off 16 bytes 22.9 instead of 33.2.
+template <int PIECES>
+__device__ __forceinline__ void store_past(char *to, const uint32_t *w) {
+    typedef uint32_t uintx4 __attribute__((ext_vector_type(4), aligned(2)));
+#pragma unroll
+    for (int h = 0; h < PIECES; ++h)
+        __builtin_nontemporal_store(uintx4{w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]},
+                                    reinterpret_cast<uintx4 *>(to) + h);
+}
+
 // Raw elements i .. i + 7; those from `left` on are 0 and not read.
 template <int T>
 __device__ __forceinline__ void load_raw(const char *base, int64_t i, int left, Raw8<T> &r) {
@@ -354,10 +366,13 @@ __device__ __forceinline__ void load_raw(const char *base, int64_t i, int left, 
     }
 }
 template <int T>
-__device__ __forceinline__ void store_raw(char *base, int64_t i, int left, const Raw8<T> &r) {
+__device__ __forceinline__ void store_raw(char *base, int64_t i, int left, const Raw8<T> &r, bool past) {
     constexpr int ES = Raw8<T>::ES;
     if (left >= 8) {
-        __builtin_memcpy(base + i * ES, r.w, 8 * ES);
+        if (past)
+            store_past<ES / 2>(base + i * ES, r.w);
+        else
+            __builtin_memcpy(base + i * ES, r.w, 8 * ES);
     } else {
 #pragma unroll
         for (int q = 0; q < 7; ++q)
@@ -370,7 +385,8 @@ __device__ __forceinline__ void store_raw(char *base, int64_t i, int left, const
     }
 }
 
-// Copies.  Nothing is computed, so fp32 rows go as 16-bit rows of twice the length would.
+// Copies.  fp32 rows go as 16-bit rows of twice the length, so that a lane's 16 bytes lie
+// beside its neighbours' (past the caches, two pieces of 16 in every 32 take 1.7 times as long).
 template <int T, int PARTS>
 __global__ __launch_bounds__(256) void gather_kernel(RowsArgs a) {
     Place p;
@@ -390,15 +406,15 @@ __global__ __launch_bounds__(256) void gather_kernel(RowsArgs a) {
         const bool kept = slot < end;
 #pragma unroll
         for (int s = 0; s < PARTS; ++s)
-            if (col[s] < a.cols) store_raw<T>(a.out, slot * a.ldo + col[s], a.cols - col[s], kept ? r[s] : zero);
+            if (col[s] < a.cols) store_raw<T>(a.out, slot * a.ldo + col[s], a.cols - col[s], kept ? r[s] : zero, a.past_caches);
     }
 }
 
-// Codes past the caches, whole 8 bytes only: 65536 rows of 4096 go in 64 instead of 84 us, as
-// the lines that the scattered scales fill, 4 bytes at a time, then stay in L2 until they
-// are whole.  (Past the caches too, the scales alone take 70 us more.)
+// Codes past the caches: 65536 rows of 4096 go in 64 instead of 84 us, as the lines that the
+// scattered scales fill, 4 bytes at a time, then stay in L2 until they are whole.  (Past
+// the caches too, the scales alone take 70 us more.)
 __device__ __forceinline__ void store_past(uint8_t *to, uint2 c) {
-    typedef uint32_t uintx2 __attribute__((ext_vector_type(2)));
+    typedef uint32_t uintx2 __attribute__((ext_vector_type(2), aligned(1)));
     __builtin_nontemporal_store(uintx2{c.x, c.y}, reinterpret_cast<uintx2 *>(to));
 }
 
@@ -489,29 +505,26 @@ __global__ __launch_bounds__(256) void combine_kernel(RowsArgs a) {
     store8<T>(a.out, p.token * a.ldo + col, left, sum);
 }
 
-// 8 values past the caches, to whole 16 bytes (16384 rows of 4096 bf16: 61 against 64 us).
+// Past the caches, 16384 rows of 4096 bf16: 61 against 64 us, of 2050 fp16: 42 against 52.
 template <int T>
 __device__ __forceinline__ void store8_past(char *base, int64_t i, const float *x) {
-    typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
+    constexpr int ES = Raw8<T>::ES;
+    uint32_t w[2 * ES];
     if constexpr (T == BAKRON_T_F32) {
-        uintx4 *to = reinterpret_cast<uintx4 *>(base + 4 * i);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            __builtin_nontemporal_store(uintx4{__float_as_uint(x[4 * h]), __float_as_uint(x[4 * h + 1]),
-                                               __float_as_uint(x[4 * h + 2]), __float_as_uint(x[4 * h + 3])},
-                                        to + h);
+        for (int q = 0; q < 8; ++q) w[q] = __float_as_uint(x[q]);
     } else {
-        __builtin_nontemporal_store(uintx4{pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]),
-                                           pack2<T>(x[6], x[7])},
-                                    reinterpret_cast<uintx4 *>(base + 2 * i));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = pack2<T>(x[2 * q], x[2 * q + 1]);
     }
+    store_past<ES / 2>(base + i * ES, w);
 }
 
 // dY[slot] = w dout[t];  dw[t][j] = <dout[t], Y[slot]>, summed over a lane's columns, the
 // lanes and the waves in a fixed order.  WAVES waves take a token.
-template <int T, int WAVES>
+template <int T, int WAVES, int AT_ONCE>
 __global__ __launch_bounds__(256) void combine_grad_kernel(RowsArgs a) {
-    __shared__ float part[4][BATCH];
+    __shared__ float part[4][AT_ONCE];
     const int lane = lane_id(), w = threadIdx.x >> 6, sub = w % WAVES;
     const int64_t at = (int64_t)blockIdx.x * (4 / WAVES) + w / WAVES;
     const bool mine = at < a.tokens;
@@ -519,33 +532,43 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(RowsArgs a) {
     const int end = rows_in_groups(a), slots = slots_of(a, token);
     const float weights = weights_of(a, token);
     const bool past = a.past_caches;
-    for (int j0 = 0; j0 < a.k; j0 += BATCH) {
-        float dot[BATCH] = {}, weight[BATCH];
-        int slot[BATCH];  // -1: none
+    for (int j0 = 0; j0 < a.k; j0 += AT_ONCE) {
+        float dot[AT_ONCE] = {};
+        int slot[AT_ONCE];  // -1: none
 #pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-            slot[j] = mine && j0 + j < a.k ? from_lane(slots, j0 + j) : -1;
-            weight[j] = from_lane(weights, (j0 + j) & 63);
-        }
-        for (int col = (sub * 64 + lane) * 8; mine && col < a.cols; col += WAVES * 512) {
+        for (int j = 0; j < AT_ONCE; ++j) slot[j] = mine && j0 + j < a.k ? from_lane(slots, j0 + j) : -1;
+        // what a turn reads is asked for in the turn before
+        Raw8<T> d, r[AT_ONCE];
+        auto load = [&](int col) {
             const int left = a.cols - col;
-            float d[8];
-            load8<T>(a.dout, token * a.ldd + col, left, d);
-            Raw8<T> r[BATCH];
+            if (left <= 0) return;
+            load_raw<T>(a.dout, token * a.ldd + col, left, d);
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j)
+            for (int j = 0; j < AT_ONCE; ++j)
                 if (slot[j] >= 0 && slot[j] < end) load_raw<T>(a.x, slot[j] * a.ldx + col, left, r[j]);
+        };
+        int col = (sub * 64 + lane) * 8;
+        if (mine) load(col);
+        for (; mine && col < a.cols; col += WAVES * 512) {
+            const int left = a.cols - col;
+            float x[8];
+            unpack8<T>(d.w, x);
+            Raw8<T> now[AT_ONCE];
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j) {
+            for (int j = 0; j < AT_ONCE; ++j) now[j] = r[j];
+            load(col + WAVES * 512);
+#pragma unroll
+            for (int j = 0; j < AT_ONCE; ++j) {
                 if (slot[j] < 0) continue;
                 float dy[8] = {};
                 if (slot[j] < end) {
+                    const float weight = from_lane(weights, (j0 + j) & 63);
                     float y[8];
-                    unpack8<T>(r[j].w, y);
+                    unpack8<T>(now[j].w, y);
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
-                        dot[j] += d[q] * y[q];
-                        dy[q] = weight[j] * d[q];
+                        dot[j] += x[q] * y[q];
+                        dy[q] = weight * x[q];
                     }
                 }
                 if (past && left >= 8)
@@ -555,21 +578,21 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(RowsArgs a) {
             }
         }
 #pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
+        for (int j = 0; j < AT_ONCE; ++j) {
             if (j0 + j >= a.k) break;
 #pragma unroll
             for (int off = 32; off > 0; off >>= 1) dot[j] += __shfl_xor(dot[j], off);
         }
         if constexpr (WAVES == 1) {
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j)
+            for (int j = 0; j < AT_ONCE; ++j)
                 if (mine && lane == 0 && j0 + j < a.k) a.dweights[token * a.k + j0 + j] = dot[j];
         } else {
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j)
+            for (int j = 0; j < AT_ONCE; ++j)
                 if (lane == 0) part[w][j] = dot[j];
             __syncthreads();
-            if (mine && sub == 0 && lane < BATCH && j0 + lane < a.k) {
+            if (mine && sub == 0 && lane < AT_ONCE && j0 + lane < a.k) {
                 float s = 0.0f;
                 for (int v = 0; v < WAVES; ++v) s += part[w + v][lane];
                 a.dweights[token * a.k + j0 + lane] = s;
@@ -590,23 +613,35 @@ void by_tokens(RowsArgs a, int64_t tokens, int64_t threads, Launch launch) {
     }
 }
 
-template <int T, int PARTS>
-void launch_gather(RowsArgs a, int64_t tokens, bool fp8, hipStream_t s) {
+template <int T, int PARTS, bool FP8>
+void launch_gather(RowsArgs a, int64_t tokens, hipStream_t s) {
     a.segs = (a.cols + 512 * PARTS - 1) / (512 * PARTS);
     by_tokens(a, tokens, (int64_t)64 * a.segs, [&](const RowsArgs &b, dim3 grid) {
-        if (fp8)
+        if constexpr (FP8)
             hipLaunchKernelGGL((gather_fp8_kernel<T, PARTS>), grid, dim3(256), 0, s, b);
         else
             hipLaunchKernelGGL((gather_kernel<T, PARTS>), grid, dim3(256), 0, s, b);
     });
 }
 
-template <int T>
-void launch_gather(const RowsArgs &a, int64_t tokens, bool fp8, hipStream_t s) {
+// Few tokens are spread over as many waves as there are pieces of 512 columns; with many a
+// wave takes two pieces (65536 fp8 rows of 4096: 63.5 us, with four 65.5).
+template <int T, bool FP8>
+void launch_gather(const RowsArgs &a, int64_t tokens, hipStream_t s) {
     if (a.cols <= 512 || tokens <= 512)
-        launch_gather<T, 1>(a, tokens, fp8, s);
+        launch_gather<T, 1, FP8>(a, tokens, s);
     else
-        launch_gather<T, 2>(a, tokens, fp8, s);
+        launch_gather<T, 2, FP8>(a, tokens, s);
+}
+
+template <int T, int WAVES>
+void launch_combine_grad(const RowsArgs &a, int64_t tokens, hipStream_t s) {
+    by_tokens(a, tokens, 64 * WAVES, [&](const RowsArgs &b, dim3 grid) {
+        if (a.k <= 4)
+            hipLaunchKernelGGL((combine_grad_kernel<T, WAVES, 4>), grid, dim3(256), 0, s, b);
+        else
+            hipLaunchKernelGGL((combine_grad_kernel<T, WAVES, BATCH>), grid, dim3(256), 0, s, b);
+    });
 }
 
 template <int T>
@@ -615,14 +650,12 @@ void launch_combine(RowsArgs a, int64_t tokens, hipStream_t s) {
         a.segs = (a.cols + 511) / 512;
         by_tokens(a, tokens, (int64_t)64 * a.segs,
                   [&](const RowsArgs &b, dim3 grid) { hipLaunchKernelGGL(combine_kernel<T>, grid, dim3(256), 0, s, b); });
+    } else if (a.cols <= 512) {
+        launch_combine_grad<T, 1>(a, tokens, s);
     } else if (a.cols <= 1024) {
-        by_tokens(a, tokens, 64, [&](const RowsArgs &b, dim3 grid) {
-            hipLaunchKernelGGL((combine_grad_kernel<T, 1>), grid, dim3(256), 0, s, b);
-        });
-    } else {
-        by_tokens(a, tokens, 256, [&](const RowsArgs &b, dim3 grid) {
-            hipLaunchKernelGGL((combine_grad_kernel<T, 4>), grid, dim3(256), 0, s, b);
-        });
+        launch_combine_grad<T, 2>(a, tokens, s);
+    } else {  // 8 waves: 16384 rows of 4096 fp16 in 74 us, of 2050 in 50
+        launch_combine_grad<T, 4>(a, tokens, s);
     }
 }
 
@@ -724,7 +757,9 @@ extern "C" int32_t bakron_group_gather(const void *X, int32_t type, int64_t toke
     RowsArgs a = {};
     a.x = static_cast<const char *>(X), a.out = static_cast<char *>(out), a.ldx = ldx, a.ldo = ldo;
     a.slots = slots, a.end = offsets + groups, a.k = k, a.cols = (int)cols, a.n = tokens * k, a.dev_status = dev_status;
-    by_type(type, [&](auto t) { launch_gather<t.value>(a, tokens, false, static_cast<hipStream_t>(stream_)); });
+    a.past_caches = many(a.n * cols * elem_size(type));
+    if (type == BAKRON_T_F32) a.cols *= 2, a.ldx *= 2, a.ldo *= 2;
+    launch_gather<BAKRON_T_BF16, false>(a, tokens, static_cast<hipStream_t>(stream_));
     BK_LAUNCH_CHECK("gather_kernel");
     return BAKRON_OK;
 }
@@ -742,9 +777,9 @@ extern "C" int32_t bakron_group_gather_fp8(const void *X, int32_t type, int64_t 
     RowsArgs a = {};
     a.x = static_cast<const char *>(X), a.out = reinterpret_cast<char *>(Q), a.ldx = ldx, a.ldo = ldq;
     a.slots = slots, a.end = offsets + groups, a.k = k, a.cols = (int)cols, a.n = tokens * k, a.scales = scales;
-    a.past_caches = many(a.n * cols) && ldq % 8 == 0 && aligned(Q, 8);
+    a.past_caches = many(a.n * cols);
     a.dev_status = dev_status;
-    by_type(type, [&](auto t) { launch_gather<t.value>(a, tokens, true, static_cast<hipStream_t>(stream_)); });
+    by_type(type, [&](auto t) { launch_gather<t.value, true>(a, tokens, static_cast<hipStream_t>(stream_)); });
     BK_LAUNCH_CHECK("gather_fp8_kernel");
     return BAKRON_OK;
 }
@@ -787,7 +822,7 @@ extern "C" int32_t bakron_group_combine_grad(const void *dout, int64_t ldd, cons
     a.x = static_cast<const char *>(Y), a.dout = static_cast<const char *>(dout), a.out = static_cast<char *>(dY);
     a.ldx = ldy, a.ldd = ldd, a.ldo = lddy, a.slots = slots, a.end = offsets + groups, a.weights = weights;
     a.dweights = dweights, a.k = k, a.cols = (int)cols, a.n = tokens * k, a.dev_status = dev_status;
-    a.past_caches = many(a.n * cols * elem_size(type)) && lddy * elem_size(type) % 16 == 0 && aligned(dY, 16);
+    a.past_caches = many(a.n * cols * elem_size(type));
     by_type(type, [&](auto t) { launch_combine<t.value>(a, tokens, static_cast<hipStream_t>(stream_)); });
     BK_LAUNCH_CHECK("combine_grad_kernel");
     return BAKRON_OK;
