@@ -230,6 +230,26 @@ def test_values_of_other_rows_and_adapters_do_not_leak(bk, rows, dtype):
         assert torch.equal(got[[0, 2, 3]], was[[0, 2, 3]]) and got[1].isnan().any()
 
 
+@pytest.mark.parametrize("rows", [30, 1500])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_infinities_of_a_matrix(bk, rows, dtype):
+    """Results that depend on a value that is not finite are not finite, all others as they were."""
+    c = Case(rows, 300, 72, 16, 2, 3, dtype, 13)
+    offsets, order, _ = bk.group_sort(c.ids.cuda(), 2)
+    X, dY, args = c.X.cuda(), c.dY.cuda(), (offsets, order)
+    clean = bk.adapter_matmul(X, c.A.cuda(), c.B.cuda(), *args)
+    grads = bk.adapter_matmul_grad(dY, X, c.A.cuda(), c.B.cuda(), *args)
+    c.B[1, 7, 3], c.B[1, 290, 15] = float("inf"), float("-inf")
+    out = bk.adapter_matmul(X, c.A.cuda(), c.B.cuda(), *args)
+    mine = (c.ids == 1).cuda()
+    assert not out[mine][:, [7, 290]].isfinite().any()
+    out[mine, 7], out[mine, 290] = clean[mine, 7], clean[mine, 290]
+    assert torch.equal(out, clean)
+    dx, da, db = bk.adapter_matmul_grad(dY, X, c.A.cuda(), c.B.cuda(), *args)
+    assert torch.equal(dx[~mine], grads[0][~mine]) and not dx[mine].isfinite().any()
+    assert not da[1, [3, 15]].isfinite().any() and torch.equal(da[0], grads[1][0]) and torch.equal(db, grads[2])
+
+
 def test_values_between_beyond_fp16(bk):
     """Rank values far beyond fp16's range, and far below it, come through."""
     rows, N, K, rank = 48, 64, 128, 16

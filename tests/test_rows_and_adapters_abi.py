@@ -108,6 +108,7 @@ def sizes_refusals(lib, call):
     refused(lib, call(groups=0), b"groups")
     refused(lib, call(groups=4097), b"groups")
     refused(lib, call(rows=1 << 24, N=1 << 24), b"too many tiles")
+    refused(lib, call(groups=4096, K=1 << 24), b"too many tiles")
     refused(lib, call(off=None, groups=2), b"offsets")
     refused(lib, call(type=0), b"type")
     refused(lib, call(type=3), b"type")

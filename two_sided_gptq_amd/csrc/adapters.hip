@@ -990,11 +990,14 @@ bool sizes_ok(int64_t rows, int64_t N, int64_t K, int32_t rank, int32_t groups) 
     if (!(rows >= 1 && N >= 1 && K >= 1 && rows <= MAX_DIM && N <= MAX_DIM && K <= MAX_DIM && rank >= 1 &&
           rank <= MAX_RANK && groups >= 1 && groups <= MAX_GROUPS))
         return false;
-    // no launch of 2^32 threads or more: the widest tiles' first dimension, in all of them
-    const int64_t most = std::max(N, K), slots = row_tiles(16, rows, groups, true) + 8;
-    return slots * 1024 <= LAUNCH_THREADS && slots * ((most + 255) / 256) * 256 <= LAUNCH_THREADS &&
-           std::max<int64_t>(groups, 1024 + groups + 1) * ((most + 127) / 128) * 256 <= LAUNCH_THREADS &&
-           ((most + 63) / 64) * ((rank + 63) / 64) * 256 <= LAUNCH_THREADS;
+    // no launch of 2^32 threads or more in a dimension; expand and outer are the widest
+    const int64_t most = std::max(N, K);
+    for (bool grad : {false, true}) {
+        const Layout y = layout_of(rows, N, K, rank, groups, grad);
+        if (y.slots * ((most + 255) / 256) * 256 > LAUNCH_THREADS) return false;
+        if (grad && y.units * ((most + 127) / 128) * 64 * OUTER_WAVES > LAUNCH_THREADS) return false;
+    }
+    return true;
 }
 
 int32_t check_common(int64_t rows, int64_t N, int64_t K, int32_t rank, int32_t groups, const int32_t *offsets,
