@@ -30,6 +30,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 constexpr int64_t MAX_DIM = int64_t(1) << 24;
 constexpr int MAX_GROUPS = 4096;
 constexpr int MAX_RANK = 256;
+constexpr int MAX_SPLITS = 8;  // workgroups that share a tile's K
 
 template <int T>
 __device__ __forceinline__ floatx4 mfma(uintx4 a, uintx4 b, floatx4 c) {
@@ -202,7 +203,7 @@ constexpr int shrink_lds(int mt, int rt) {
 
 // GRAD: matrices of either order.
 template <int T, int MT, int RT, bool GRAD>
-__global__ __launch_bounds__(64 * shrink_waves(MT, RT), GRAD && MT * RT == 8 ? 2 : 4) void shrink_kernel(ShrinkArgs a) {
+__global__ __launch_bounds__(64 * shrink_waves(MT, RT), 4) void shrink_kernel(ShrinkArgs a) {
     extern __shared__ __align__(16) float space[];
     const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
     constexpr int waves = shrink_waves(MT, RT), KS = SHRINK_STEP, DEPTH = MT * RT == 1 ? 3 : MT * RT == 2 ? 2 : 1;
@@ -430,22 +431,39 @@ __device__ __forceinline__ void add_products(const uintx4 &f, const uintx4 &hi, 
     }
 }
 
-// P of the tile's places to LDS, rows of `ranks` 4 words apart.
-__device__ __forceinline__ void stage_p(const ExpandArgs &a, int64_t sub, int count, uint32_t *lds) {
-    const uint32_t *p = a.p + sub * 16 * a.ranks;
-    const int words = (count + 15) / 16 * 16 * a.ranks;
-    for (int i = threadIdx.x * 4; i < words; i += 1024) {
-        const int r = i / a.ranks, c = i - r * a.ranks;
-        uintx4 v = *reinterpret_cast<const uintx4 *>(p + i);
-        if (a.splits > 1) {
-            floatx4 sum = __builtin_bit_cast(floatx4, v);
-            for (int k = 1; k < a.splits; ++k) sum += *reinterpret_cast<const floatx4 *>(p + k * a.part_words + i);
+// P of the tile's places, on its way from memory, 16 bytes a thread and turn; then to LDS,
+// rows of `ranks` 4 words apart.
+template <int MT, int RS>
+struct StagedP {
+    static constexpr int TURNS = (MT * RS + 1) / 2;
+    uintx4 v[TURNS];
+    __device__ __forceinline__ void load(const ExpandArgs &a, int64_t slot, int words) {
+        const uint32_t *p = a.p + slot * MT * 16 * a.ranks;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = pack_parts(sum[e]);
+        for (int k = 0; k < TURNS; ++k) {
+            const int i = k * 1024 + threadIdx.x * 4;
+            if (i < words) v[k] = *reinterpret_cast<const uintx4 *>(p + i);
         }
-        *reinterpret_cast<uintx4 *>(lds + r * (a.ranks + 4) + c) = v;
+        if (MT > 1 || a.splits == 1) return;
+#pragma unroll
+        for (int k = 0; k < TURNS; ++k) {
+            const int i = k * 1024 + threadIdx.x * 4;
+            if (i >= words) break;
+            floatx4 sum = __builtin_bit_cast(floatx4, v[k]);
+#pragma unroll 1
+            for (int m = 1; m < a.splits; ++m) sum += *reinterpret_cast<const floatx4 *>(p + m * a.part_words + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[k][e] = pack_parts(sum[e]);
+        }
     }
-}
+    __device__ __forceinline__ void store(const ExpandArgs &a, int words, uint32_t *lds) const {
+#pragma unroll
+        for (int k = 0; k < TURNS; ++k) {
+            const int i = k * 1024 + threadIdx.x * 4, r = i / a.ranks;
+            if (i < words) *reinterpret_cast<uintx4 *>(lds + r * (a.ranks + 4) + (i - r * a.ranks)) = v[k];
+        }
+    }
+};
 
 __device__ __forceinline__ void p_frags(const ExpandArgs &a, const uint32_t *lds, int place, int r, uintx4 &hi, uintx4 &lo) {
     uint32_t p[8] = {};
@@ -463,6 +481,9 @@ __device__ __forceinline__ void expand_whole(const ExpandArgs &a, const Tile &t,
     const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4, lr = lane >> 3, lc = lane & 7;
     const bool none = t.g == a.of.groups;
     const int count = t.p1 - t.p0;
+    const int words = none ? 0 : (count + 15) / 16 * 16 * a.ranks;
+    StagedP<MT, RS> p;
+    p.load(a, slot, words);
     int row[MT][2];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -503,7 +524,7 @@ __device__ __forceinline__ void expand_whole(const ExpandArgs &a, const Tile &t,
             base[i][h] = Raw8<OT>{};
             if (a.base) __builtin_memcpy(base[i][h].w, a.base + OS * (max(row[i][h], 0) * a.ldb + n0 + lc * 8), 8 * OS);
         }
-    if (!none) stage_p(a, slot * MT, count, lds);
+    p.store(a, words, lds);
     __syncthreads();
     uintx4 f[4][RS];
     if constexpr (!STRIDED) {
@@ -607,7 +628,10 @@ __device__ __forceinline__ void expand_any(const ExpandArgs &a, const Tile &t, i
             }
         }
     }
-    if (!none) stage_p(a, slot * MT, count, lds);
+    StagedP<MT, RS> p;
+    const int words = none ? 0 : (count + 15) / 16 * 16 * a.ranks;
+    p.load(a, slot, words);
+    p.store(a, words, lds);
     __syncthreads();
     for (int i = 0; i * 16 < count; ++i) {
         const int row = i * 16 + l < count ? a.rows[slot * (16 * MT) + i * 16 + l] : -1;
@@ -669,7 +693,7 @@ struct Outer {
     int cols;               // K or N
     const uint32_t *g;      // by_rank
     char *out;
-    int64_t ldo, group_o;   // elements
+    int64_t group_o;        // elements
     int by_column;          // dB: a row of `out` is one column of Z
     int64_t part0;          // first element of the job's partial sums in a unit's
 };
@@ -692,21 +716,11 @@ __device__ __forceinline__ void store_any(char *base, int type, int64_t i, int l
     else
         store8<BAKRON_T_F16>(base, i, left, x);
 }
-__device__ __forceinline__ void store_any1(char *base, int type, int64_t i, float x) {
-    if (type == BAKRON_T_F32)
-        store1<BAKRON_T_F32>(base, i, x);
-    else if (type == BAKRON_T_BF16)
-        store1<BAKRON_T_BF16>(base, i, x);
-    else
-        store1<BAKRON_T_F16>(base, i, x);
-}
-
 // A workgroup takes a unit's places, 128 columns and 16 RT ranks; its waves share the
 // places, 32 at a time.  A lane reads 8 columns of 8 rows and turns them about with byte
-// permutes: the matrix cores want 8 places of one column.
-constexpr int OUTER_WAVES = 8;
-
-template <int T, int RT, bool WHOLE>
+// permutes: the matrix cores want 8 places of one column.  The waves are as many as a usual
+// unit has turns for (64 groups of 62 rows: 8 waves NN us, 2 waves NN).
+template <int T, int WAVES, int RT, bool WHOLE>
 __device__ __forceinline__ void outer_sum(const OuterArgs &a, const Outer &job, const Tile &t, int64_t sub, int c0, int r0,
                                           floatx4 (&acc)[8][RT]) {
     const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
@@ -714,9 +728,9 @@ __device__ __forceinline__ void outer_sum(const OuterArgs &a, const Outer &job, 
     const int col = c0 + l * 8, left = job.cols - col, count = t.p1 - t.p0;
     // the rows of the next 32 places, one a lane
     int next = row_at(a.of, t.p0 + w * 32 + (lane & 31), t.p1);
-    for (int s = w * 32; s < count; s += OUTER_WAVES * 32) {
+    for (int s = w * 32; s < count; s += WAVES * 32) {
         const int row = next;
-        next = row_at(a.of, t.p0 + s + OUTER_WAVES * 32 + (lane & 31), t.p1);
+        next = row_at(a.of, t.p0 + s + WAVES * 32 + (lane & 31), t.p1);
         uintx4 v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -759,9 +773,13 @@ __device__ __forceinline__ void outer_sum(const OuterArgs &a, const Outer &job, 
     }
 }
 
-template <int T, int RT>
-__global__ __launch_bounds__(64 * OUTER_WAVES) void outer_kernel(OuterArgs a) {
-    __shared__ __align__(16) floatx4 space[OUTER_WAVES / 2 * 8 * RT * 64];
+template <int T, int WAVES, int RT>
+__global__ __launch_bounds__(64 * WAVES) void outer_kernel(OuterArgs a) {
+    // half of the waves' sums; then the results as rows of the output
+    constexpr int HALF = WAVES / 2 * 8 * RT * 256, BY_RANK = 128 + 4, BY_COLUMN = 16 * RT + 4;
+    constexpr int RESULTS = BY_RANK * 16 * RT > BY_COLUMN * 128 ? BY_RANK * 16 * RT : BY_COLUMN * 128;
+    __shared__ __align__(16) float room[HALF > RESULTS ? HALF : RESULTS];
+    floatx4 *space = reinterpret_cast<floatx4 *>(room);
     const Outer &job = a.job[blockIdx.z];
     const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -795,12 +813,12 @@ __global__ __launch_bounds__(64 * OUTER_WAVES) void outer_kernel(OuterArgs a) {
 #pragma unroll
         for (int r = 0; r < RT; ++r) acc[c][r] = floatx4{0, 0, 0, 0};
     if (c0 + 128 <= job.cols)
-        outer_sum<T, RT, true>(a, job, t, sub, c0, r0, acc);
+        outer_sum<T, WAVES, RT, true>(a, job, t, sub, c0, r0, acc);
     else
-        outer_sum<T, RT, false>(a, job, t, sub, c0, r0, acc);
+        outer_sum<T, WAVES, RT, false>(a, job, t, sub, c0, r0, acc);
     // the upper half of the waves to the lower, until one is left
 #pragma unroll
-    for (int half = OUTER_WAVES / 2; half > 0; half >>= 1) {
+    for (int half = WAVES / 2; half > 0; half >>= 1) {
         if (w >= half && w < 2 * half)
 #pragma unroll
             for (int c = 0; c < 8; ++c)
@@ -814,53 +832,53 @@ __global__ __launch_bounds__(64 * OUTER_WAVES) void outer_kernel(OuterArgs a) {
                 for (int r = 0; r < RT; ++r) acc[c][r] += space[((w * 8 + c) * RT + r) * 64 + lane];
         __syncthreads();
     }
-    if (w != 0) return;
     // lane: rank l, columns 8 (4 q + e) + c
+    if (w == 0) {
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const int rank = r0 + r * 16 + l;
-        if (rank >= a.rank) continue;
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int at = c0 + 8 * (4 * q + e);
-            float x[8];
+            for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int c = 0; c < 8; ++c) x[c] = acc[c][r][e];
-            if (a.chunk) {
-                store8<BAKRON_T_F32>(reinterpret_cast<char *>(a.part), unit * a.part_size + job.part0 + (int64_t)rank * job.cols + at,
-                                     job.cols - at, x);
-            } else if (!job.by_column) {
-                store_any(job.out, a.otype, t.g * job.group_o + rank * job.ldo + at, job.cols - at, x);
-            } else {
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    if (at + c < job.cols) store_any1(job.out, a.otype, t.g * job.group_o + (at + c) * job.ldo + rank, x[c]);
-            }
-        }
+                for (int c = 0; c < 8; ++c) {
+                    const int rank = r * 16 + l, at = 8 * (4 * q + e) + c;
+                    room[job.by_column ? at * BY_COLUMN + rank : rank * BY_RANK + at] = acc[c][r][e];
+                }
+    }
+    __syncthreads();
+    // the output's rows: of a rank, or of a column; a group's are contiguous
+    const int length = job.by_column ? 16 * RT : 128, rows = job.by_column ? 128 : 16 * RT, pitch = job.by_column ? BY_COLUMN : BY_RANK;
+    const int row0 = job.by_column ? c0 : r0, col1 = job.by_column ? r0 : c0;
+    const int all_rows = job.by_column ? job.cols : a.rank, all_cols = job.by_column ? a.rank : job.cols;
+    for (int i = threadIdx.x * 8; i < rows * length; i += 64 * WAVES * 8) {
+        const int y = i / length, x = i - y * length, left = all_cols - (col1 + x);
+        if (row0 + y >= all_rows || left <= 0) continue;
+        const float *v = room + y * pitch + x;
+        const int64_t at = (int64_t)(row0 + y) * all_cols + col1 + x;
+        if (a.chunk)
+            store8<BAKRON_T_F32>(reinterpret_cast<char *>(a.part), unit * a.part_size + job.part0 + at, left, v);
+        else
+            store_any(job.out, a.otype, t.g * job.group_o + at, left, v);
     }
 }
 
-// Adds a group's units, in order.  A thread takes 8 columns of a rank.
+// Adds a group's units, in order.  A thread takes 8 neighbours.
 __global__ __launch_bounds__(256) void outer_join_kernel(OuterArgs a) {
     const Outer &job = a.job[blockIdx.z];
-    const int g = blockIdx.y, per_row = (job.cols + 7) / 8;
+    const int g = blockIdx.y, lane = threadIdx.x & 63;
     int first = 0;
-    const int lane = threadIdx.x & 63;
+    int64_t p, z;
     for (int e = lane; e < g; e += 64) {
-        int64_t p, z;
         rows_of_group(a.of.offsets, a.of.groups, a.of.rows, e, p, z);
-        first += (int)((z - p + a.chunk - 1) / a.chunk);
+        first += ((int)(z - p) + a.chunk - 1) / a.chunk;
     }
     first = __builtin_amdgcn_readlane(wave_scan(first), 63);
-    int64_t p, z;
     rows_of_group(a.of.offsets, a.of.groups, a.of.rows, g, p, z);
-    const int last = min(a.units, first + (int)((z - p + a.chunk - 1) / a.chunk));
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)a.rank * per_row) return;
-    const int rank = (int)(i / per_row), col = (int)(i - (int64_t)rank * per_row) * 8, left = job.cols - col;
+    const int last = min(a.units, first + ((int)(z - p) + a.chunk - 1) / a.chunk);
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8, left = (int64_t)a.rank * job.cols - i;
+    if (left <= 0) return;
     float sum[8] = {};
-    const char *from = reinterpret_cast<const char *>(a.part + job.part0 + (int64_t)rank * job.cols + col);
-    for (int u0 = first; u0 < last; u0 += 4) {
+    const char *from = reinterpret_cast<const char *>(a.part + job.part0 + i);
+    for (int u0 = max(first, 0); u0 < last; u0 += 4) {
         float x[4][8] = {};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -870,12 +888,7 @@ __global__ __launch_bounds__(256) void outer_join_kernel(OuterArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[e] += x[k][e];
     }
-    if (!job.by_column) {
-        store_any(job.out, a.otype, g * job.group_o + rank * job.ldo + col, left, sum);
-    } else {
-        for (int e = 0; e < 8 && e < left; ++e)
-            store_any1(job.out, a.otype, g * job.group_o + (col + e) * job.ldo + rank, sum[e]);
-    }
+    store_any(job.out, a.otype, g * job.group_o + i, (int)min<int64_t>(left, 8), sum);
 }
 
 // ---------------------------------------------------------------- layout and launches
@@ -889,6 +902,7 @@ struct Layout {
     int splits;             // of K, in shrink
     int chunk;              // of the sums over places; 0: a group is one unit
     int64_t units;
+    int outer_waves;        // waves that share a unit's places
 };
 
 // Places that a workgroup of shrink takes, in 16s.
@@ -901,25 +915,28 @@ Layout layout_of(int64_t rows, int64_t N, int64_t K, int32_t rank, int32_t group
     y.mt = rows >= 64 * (int64_t)(groups + 1) && rows >= 1024 ? 4 : 1;
     y.slots = row_tiles(16 * y.mt, rows, groups, true);
     const int blocks = y.ranks / 16;
-    y.rt = y.mt == 1 && y.slots * blocks <= 1024 ? 1 : blocks >= 4 ? 4 : blocks >= 2 ? 2 : 1;
+    // Gradients take 32 ranks at once at most: with 64 and both orders of a matrix the registers
+    // leave one workgroup a CU (8192 rows, rank 128, 4096 x 4096: NN against NN us).
+    y.rt = y.mt == 1 && y.slots * blocks <= 1024 ? 1 : blocks >= 4 && !grad ? 4 : blocks >= 2 ? 2 : 1;
     // Where CUs idle, several workgroups share a tile's K, 2 steps a wave at least (8 rows of
     // their own adapters, rank 16, K = 14336: 10.3 us, unshared 14.9; 64 rows, K = 4096: 10.9 and
     // 11.9).
     y.splits = 1;
     if (!grad && y.mt == 1 && y.rt == 1)
-        while (y.splits < 8 && y.slots * blocks * y.splits * 2 <= 256 && K >= (int64_t)SHRINK_STEP * 16 * 2 * y.splits * 2) y.splits *= 2;
+        while (y.splits < MAX_SPLITS && y.slots * blocks * y.splits * 2 <= 256 && K >= (int64_t)SHRINK_STEP * 16 * 2 * y.splits * 2) y.splits *= 2;
     y.chunk = 0;
     y.units = groups;
     // Sums over places: a group at a time, or, where that leaves CUs idle and there are places
-    // enough to pay for joining, chunks of a group.
+    // enough to pay for joining, chunks of a group.  A CU holds two workgroups, one of 64 ranks.
     if (grad) {
-        const int64_t tiles = (N + 127) / 128 + (K + 127) / 128, want = 512;
+        const int64_t tiles = ((N + 127) / 128 + (K + 127) / 128) * ((blocks + 3) / 4), want = blocks >= 3 ? 256 : 512;
         if (tiles * groups < want && rows > 2048) {
             const int64_t splits = (want + tiles - 1) / tiles;
             y.chunk = (int)std::max<int64_t>(512, round_up((rows + splits - 1) / splits, 128));
             y.units = row_tiles(y.chunk, rows, groups, true);
         }
     }
+    y.outer_waves = rows <= 128 * (int64_t)groups ? 2 : 8;
     return y;
 }
 
@@ -928,10 +945,13 @@ size_t place_words(const Layout &y) { return (size_t)y.slots * y.mt * 16 * y.ran
 template <int T, int MT, int RT>
 void launch_shrink(const ShrinkArgs &a, const Layout &y, int deep, hipStream_t s) {
     const dim3 grid((unsigned)(round_up(y.slots, 8) * (y.mt / MT)), (unsigned)((y.ranks / 16 + RT - 1) / RT), deep);
-    if (a.job[0].strided)
-        hipLaunchKernelGGL((shrink_kernel<T, MT, RT, true>), grid, dim3(64 * shrink_waves(MT, RT)), shrink_lds(MT, RT), s, a);
-    else
-        hipLaunchKernelGGL((shrink_kernel<T, MT, RT, false>), grid, dim3(64 * shrink_waves(MT, RT)), shrink_lds(MT, RT), s, a);
+    const dim3 block(64 * shrink_waves(MT, RT));
+    if constexpr (RT < 4)  // the gradients' layout has no more
+        if (a.job[0].strided) {
+            hipLaunchKernelGGL((shrink_kernel<T, MT, RT, true>), grid, block, shrink_lds(MT, RT), s, a);
+            return;
+        }
+    hipLaunchKernelGGL((shrink_kernel<T, MT, RT, false>), grid, block, shrink_lds(MT, RT), s, a);
 }
 template <int T>
 void launch_shrink(ShrinkArgs a, const Layout &y, int deep, hipStream_t s) {
@@ -967,19 +987,23 @@ void launch_expand(const ExpandArgs &a, int32_t otype, const Layout &y, hipStrea
         y.mt == 1 ? launch_expand<T, T, 1, STRIDED>(a, y, s) : launch_expand<T, T, 4, STRIDED>(a, y, s);
 }
 
-template <int T>
+template <int T, int WAVES>
 void launch_outer(const OuterArgs &a, const Layout &y, hipStream_t s) {
     const int64_t across = (std::max(a.job[0].cols, a.job[1].cols) + 127) / 128;
     const int blocks = y.ranks / 16;
     const unsigned x = (unsigned)(across * a.units);
     if (blocks == 1)
-        hipLaunchKernelGGL((outer_kernel<T, 1>), dim3(x, 1, 2), dim3(64 * OUTER_WAVES), 0, s, a);
+        hipLaunchKernelGGL((outer_kernel<T, WAVES, 1>), dim3(x, 1, 2), dim3(64 * WAVES), 0, s, a);
     else if (blocks == 2)
-        hipLaunchKernelGGL((outer_kernel<T, 2>), dim3(x, 1, 2), dim3(64 * OUTER_WAVES), 0, s, a);
+        hipLaunchKernelGGL((outer_kernel<T, WAVES, 2>), dim3(x, 1, 2), dim3(64 * WAVES), 0, s, a);
     else
-        hipLaunchKernelGGL((outer_kernel<T, 4>), dim3(x, (unsigned)((blocks + 3) / 4), 2), dim3(64 * OUTER_WAVES), 0, s, a);
+        hipLaunchKernelGGL((outer_kernel<T, WAVES, 4>), dim3(x, (unsigned)((blocks + 3) / 4), 2), dim3(64 * WAVES), 0, s, a);
+}
+template <int T>
+void launch_outer(const OuterArgs &a, const Layout &y, hipStream_t s) {
+    y.outer_waves == 2 ? launch_outer<T, 2>(a, y, s) : launch_outer<T, 8>(a, y, s);
     if (a.chunk) {
-        const int64_t threads = a.rank * across * 16;
+        const int64_t threads = (a.rank * (int64_t)std::max(a.job[0].cols, a.job[1].cols) + 7) / 8;
         hipLaunchKernelGGL(outer_join_kernel, dim3((unsigned)((threads + 255) / 256), a.of.groups, 2), dim3(256), 0, s, a);
     }
 }
@@ -995,7 +1019,7 @@ bool sizes_ok(int64_t rows, int64_t N, int64_t K, int32_t rank, int32_t groups) 
     for (bool grad : {false, true}) {
         const Layout y = layout_of(rows, N, K, rank, groups, grad);
         if (y.slots * ((most + 255) / 256) * 256 > LAUNCH_THREADS) return false;
-        if (grad && y.units * ((most + 127) / 128) * 64 * OUTER_WAVES > LAUNCH_THREADS) return false;
+        if (grad && y.units * ((most + 127) / 128) * 64 * y.outer_waves > LAUNCH_THREADS) return false;
     }
     return true;
 }
@@ -1161,8 +1185,8 @@ extern "C" int32_t bakron_adapter_matmul_grad(const void *dY, int64_t lddy, cons
         o.of = of, o.rank = rank, o.ranks = y.ranks, o.high = 16 * y.mt, o.chunk = y.chunk, o.units = (int)y.units;
         o.subs = y.slots * y.mt;
         o.otype = wtype, o.part = part, o.part_size = (int64_t)rank * (N + K);
-        o.job[0] = {x, ldx, (int)K, ur, static_cast<char *>(dA), K, rank * K, 0, 0};
-        o.job[1] = {dy, lddy, (int)N, pr, static_cast<char *>(dB), rank, N * rank, 1, rank * K};
+        o.job[0] = {x, ldx, (int)K, ur, static_cast<char *>(dA), rank * K, 0, 0};
+        o.job[1] = {dy, lddy, (int)N, pr, static_cast<char *>(dB), N * rank, 1, rank * K};
         type == BAKRON_T_BF16 ? launch_outer<BAKRON_T_BF16>(o, y, s) : launch_outer<BAKRON_T_F16>(o, y, s);
     }
     if (dX) {
