@@ -719,7 +719,8 @@ __device__ __forceinline__ void store_any(char *base, int type, int64_t i, int l
 // A workgroup takes a unit's places, 128 columns and 16 RT ranks; its waves share the
 // places, 32 at a time.  A lane reads 8 columns of 8 rows and turns them about with byte
 // permutes: the matrix cores want 8 places of one column.  The waves are as many as a usual
-// unit has turns for (64 groups of 62 rows: 8 waves NN us, 2 waves NN).
+// unit has turns for (gradients of 4000 rows by 64 groups, 4096 x 4096: 63 us with 2 waves, 84
+// with 8).
 template <int T, int WAVES, int RT, bool WHOLE>
 __device__ __forceinline__ void outer_sum(const OuterArgs &a, const Outer &job, const Tile &t, int64_t sub, int c0, int r0,
                                           floatx4 (&acc)[8][RT]) {
@@ -916,7 +917,7 @@ Layout layout_of(int64_t rows, int64_t N, int64_t K, int32_t rank, int32_t group
     y.slots = row_tiles(16 * y.mt, rows, groups, true);
     const int blocks = y.ranks / 16;
     // Gradients take 32 ranks at once at most: with 64 and both orders of a matrix the registers
-    // leave one workgroup a CU (8192 rows, rank 128, 4096 x 4096: NN against NN us).
+    // leave one workgroup a CU (8192 rows, rank 128, 4096 x 4096: 250 against 261 us).
     y.rt = y.mt == 1 && y.slots * blocks <= 1024 ? 1 : blocks >= 4 && !grad ? 4 : blocks >= 2 ? 2 : 1;
     // Where CUs idle, several workgroups share a tile's K, 2 steps a wave at least (8 rows of
     // their own adapters, rank 16, K = 14336: 10.3 us, unshared 14.9; 64 rows, K = 4096: 10.9 and

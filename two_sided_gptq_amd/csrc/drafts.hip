@@ -124,11 +124,11 @@ __device__ __forceinline__ double wave_sum(double s) {
     return s;
 }
 
-// The wave's sum of the weights of tokens [lo, hi): steps of 512, the loads of 4 on their
-// way together.
+// The wave's sum of the weights of tokens [lo, hi): steps of 512, the loads of some on
+// their way together.
 template <int T>
 __device__ __forceinline__ double stretch_sum(const Row &r, int lo, int hi) {
-    constexpr int U = 4, ES = Raw8<T>::ES;
+    constexpr int ES = Raw8<T>::ES, U = 8 / ES;  // in fp32 the registers hold 2
     double s = 0.0;
     const int lane = threadIdx.x & 63, steps = (hi - lo) / 512;
     const char *p = r.p + (r.at_p + lo + lane * 8) * ES, *q = r.q ? r.q + (r.at_q + lo + lane * 8) * ES : nullptr;

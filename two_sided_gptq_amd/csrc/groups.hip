@@ -301,7 +301,8 @@ __device__ __forceinline__ int rows_in_groups(const RowsArgs &a) {
 
 __device__ __forceinline__ int wave_uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// A wave takes PARTS x 512 columns (8 a lane) of a token.
+// A wave takes 512 columns (8 a lane) of a token: the more waves the better, also with many
+// tokens (16384 tokens by 4, 4096 columns fp16: 118 us, with two pieces a wave 127, with four 130).
 struct Place {
     int64_t token;
     int seg;
@@ -335,8 +336,8 @@ __device__ __forceinline__ float from_lane(float x, int lane) {
 }
 
 // PIECES x 16 bytes past the caches.  What is written once and is more than the L2s hold
-// would only push out what is read: copies of 4096 rows to 16384 of 2048 fp16 in 20.3
-// instead of 28.9 us, with rows off 16 bytes 22.9 instead of 33.2.
+// would only push out what is read: copies of 4096 rows to 16384 of 4096 fp16 in 27.4 instead of
+// 33.1 us.
 template <int PIECES>
 __device__ __forceinline__ void store_past(char *to, const uint32_t *w) {
     typedef uint32_t uintx4 __attribute__((ext_vector_type(4), aligned(2)));
@@ -387,30 +388,26 @@ __device__ __forceinline__ void store_raw(char *base, int64_t i, int left, const
 
 // Copies.  fp32 rows go as 16-bit rows of twice the length, so that a lane's 16 bytes lie
 // beside its neighbours' (past the caches, two pieces of 16 in every 32 take 1.7 times as long).
-template <int T, int PARTS>
 __global__ __launch_bounds__(256) void gather_kernel(RowsArgs a) {
+    constexpr int T = BAKRON_T_BF16;
     Place p;
     if (!place_of_wave(a, p)) return;
     const int end = rows_in_groups(a), slots = slots_of(a, p.token);
-    int col[PARTS];
-    Raw8<T> r[PARTS];
-#pragma unroll
-    for (int s = 0; s < PARTS; ++s) {
-        col[s] = (p.seg * PARTS + s) * 512 + lane_id() * 8;
-        if (col[s] < a.cols) load_raw<T>(a.x, p.token * a.ldx + col[s], a.cols - col[s], r[s]);
-    }
-    const Raw8<T> zero = {};
+    const int col = p.seg * 512 + lane_id() * 8, left = a.cols - col;
+    Raw8<T> r;
+    load_raw<T>(a.x, p.token * a.ldx + col, left, r);
     for (int j = 0; j < a.k; ++j) {
         const int slot = from_lane(slots, j);
         if (slot < 0) continue;
-        const bool kept = slot < end;
+        const uint32_t kept = slot < end ? ~0u : 0u;
+        Raw8<T> c;
 #pragma unroll
-        for (int s = 0; s < PARTS; ++s)
-            if (col[s] < a.cols) store_raw<T>(a.out, slot * a.ldo + col[s], a.cols - col[s], kept ? r[s] : zero, a.past_caches);
+        for (int q = 0; q < 4; ++q) c.w[q] = r.w[q] & kept;
+        store_raw<T>(a.out, slot * a.ldo + col, left, c, a.past_caches);
     }
 }
 
-// Codes past the caches: 65536 rows of 4096 go in 64 instead of 84 us, as the lines that the
+// Codes past the caches: 65536 rows of 4096 go in 57 instead of 76 us, as the lines that the
 // scattered scales fill, 4 bytes at a time, then stay in L2 until they are whole.  (Past
 // the caches too, the scales alone take 70 us more.)
 __device__ __forceinline__ void store_past(uint8_t *to, uint2 c) {
@@ -421,54 +418,38 @@ __device__ __forceinline__ void store_past(uint8_t *to, uint2 c) {
 // Copies in fp8: 16 lanes hold a block of 128 columns, so its maximum stays inside a
 // DPP row; each block is rounded once for all its copies.  A dropped row gets codes 0 and
 // scales 1, as a row of zeros would.
-template <int T, int PARTS>
+template <int T>
 __global__ __launch_bounds__(256) void gather_fp8_kernel(RowsArgs a) {
     Place p;
     if (!place_of_wave(a, p)) return;
     const int end = rows_in_groups(a), slots = slots_of(a, p.token);
-    float x[PARTS][8];
-    int col[PARTS];
+    const int col = p.seg * 512 + lane_id() * 8, left = a.cols - col;
+    float x[8];
+    load8<T>(a.x, p.token * a.ldx + col, left, x);
+    uint32_t m = 0;
 #pragma unroll
-    for (int s = 0; s < PARTS; ++s) {
-        col[s] = (p.seg * PARTS + s) * 512 + lane_id() * 8;
-        load8<T>(a.x, p.token * a.ldx + col[s], a.cols - col[s], x[s]);
-    }
-    uint2 code[PARTS];
-    float scale[PARTS];
-    bool any_bad = false;
-#pragma unroll
-    for (int s = 0; s < PARTS; ++s) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(x[s][q]) & 0x7fffffffu);
-        m = row_max(m);
-        float inv;
-        bool bad;
-        block_scale(m, scale[s], inv, bad);
-        any_bad |= bad;
-        code[s] = encode8(x[s], inv, bad);
-    }
-    bool used = false;
-    const bool past = a.past_caches;
+    for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(x[q]) & 0x7fffffffu);
+    m = row_max(m);
+    float scale, inv;
+    bool bad, used = false;
+    block_scale(m, scale, inv, bad);
+    const uint2 code = encode8(x, inv, bad);
     uint8_t *out = reinterpret_cast<uint8_t *>(a.out);
     for (int j = 0; j < a.k; ++j) {
         const int slot = from_lane(slots, j);
         if (slot < 0) continue;
         const bool kept = slot < end;
         used |= kept;
-#pragma unroll
-        for (int s = 0; s < PARTS; ++s)
-            if (col[s] < a.cols) {
-                uint8_t *to = out + slot * a.ldo + col[s];
-                const uint2 c = kept ? code[s] : make_uint2(0, 0);
-                if (past && col[s] + 8 <= a.cols)
-                    store_past(to, c);
-                else
-                    store8(to, c, min(8, a.cols - col[s]));
-                if ((lane_id() & 15) == 0) a.scales[(int64_t)(col[s] >> 7) * a.n + slot] = kept ? scale[s] : 1.0f;
-            }
+        if (left <= 0) continue;
+        uint8_t *to = out + slot * a.ldo + col;
+        const uint2 c = kept ? code : make_uint2(0, 0);
+        if (a.past_caches && left >= 8)
+            store_past(to, c);
+        else
+            store8(to, c, min(8, left));
+        if ((lane_id() & 15) == 0) a.scales[(int64_t)(col >> 7) * a.n + slot] = kept ? scale : 1.0f;
     }
-    if (any_bad && used && a.dev_status) atomicOr(a.dev_status, BAKRON_DEV_NONFINITE);
+    if (bad && used && a.dev_status) atomicOr(a.dev_status, BAKRON_DEV_NONFINITE);
 }
 
 constexpr int BATCH = 8;  // rows of a token in flight
@@ -505,7 +486,7 @@ __global__ __launch_bounds__(256) void combine_kernel(RowsArgs a) {
     store8<T>(a.out, p.token * a.ldo + col, left, sum);
 }
 
-// Past the caches, 16384 rows of 4096 bf16: 61 against 64 us, of 2050 fp16: 42 against 52.
+// Past the caches, 16384 rows of 4096 fp16: 62 against 65 us, of 2050: 39 against 50.
 template <int T>
 __device__ __forceinline__ void store8_past(char *base, int64_t i, const float *x) {
     constexpr int ES = Raw8<T>::ES;
@@ -613,25 +594,11 @@ void by_tokens(RowsArgs a, int64_t tokens, int64_t threads, Launch launch) {
     }
 }
 
-template <int T, int PARTS, bool FP8>
-void launch_gather(RowsArgs a, int64_t tokens, hipStream_t s) {
-    a.segs = (a.cols + 512 * PARTS - 1) / (512 * PARTS);
-    by_tokens(a, tokens, (int64_t)64 * a.segs, [&](const RowsArgs &b, dim3 grid) {
-        if constexpr (FP8)
-            hipLaunchKernelGGL((gather_fp8_kernel<T, PARTS>), grid, dim3(256), 0, s, b);
-        else
-            hipLaunchKernelGGL((gather_kernel<T, PARTS>), grid, dim3(256), 0, s, b);
-    });
-}
-
-// Few tokens are spread over as many waves as there are pieces of 512 columns; with many a
-// wave takes two pieces (65536 fp8 rows of 4096: 63.5 us, with four 65.5).
-template <int T, bool FP8>
-void launch_gather(const RowsArgs &a, int64_t tokens, hipStream_t s) {
-    if (a.cols <= 512 || tokens <= 512)
-        launch_gather<T, 1, FP8>(a, tokens, s);
-    else
-        launch_gather<T, 2, FP8>(a, tokens, s);
+// A wave for each 512 columns of a token.
+template <class Launch>
+void by_pieces(RowsArgs a, int64_t tokens, Launch launch) {
+    a.segs = (a.cols + 511) / 512;
+    by_tokens(a, tokens, (int64_t)64 * a.segs, launch);
 }
 
 template <int T, int WAVES>
@@ -647,8 +614,7 @@ void launch_combine_grad(const RowsArgs &a, int64_t tokens, hipStream_t s) {
 template <int T>
 void launch_combine(RowsArgs a, int64_t tokens, hipStream_t s) {
     if (!a.dout) {
-        a.segs = (a.cols + 511) / 512;
-        by_tokens(a, tokens, (int64_t)64 * a.segs,
+        by_pieces(a, tokens,
                   [&](const RowsArgs &b, dim3 grid) { hipLaunchKernelGGL(combine_kernel<T>, grid, dim3(256), 0, s, b); });
     } else if (a.cols <= 512) {
         launch_combine_grad<T, 1>(a, tokens, s);
@@ -757,9 +723,12 @@ extern "C" int32_t bakron_group_gather(const void *X, int32_t type, int64_t toke
     RowsArgs a = {};
     a.x = static_cast<const char *>(X), a.out = static_cast<char *>(out), a.ldx = ldx, a.ldo = ldo;
     a.slots = slots, a.end = offsets + groups, a.k = k, a.cols = (int)cols, a.n = tokens * k, a.dev_status = dev_status;
-    a.past_caches = many(a.n * cols * elem_size(type));
+    // rows off 16 bytes leave parts of lines (16384 rows of 2050 fp16: 18.5 past the caches, 15.6 else)
+    a.past_caches = many(a.n * cols * elem_size(type)) && ldo * elem_size(type) % 16 == 0 && aligned(out, 16);
     if (type == BAKRON_T_F32) a.cols *= 2, a.ldx *= 2, a.ldo *= 2;
-    launch_gather<BAKRON_T_BF16, false>(a, tokens, static_cast<hipStream_t>(stream_));
+    by_pieces(a, tokens, [&](const RowsArgs &b, dim3 grid) {
+        hipLaunchKernelGGL(gather_kernel, grid, dim3(256), 0, static_cast<hipStream_t>(stream_), b);
+    });
     BK_LAUNCH_CHECK("gather_kernel");
     return BAKRON_OK;
 }
@@ -779,7 +748,11 @@ extern "C" int32_t bakron_group_gather_fp8(const void *X, int32_t type, int64_t 
     a.slots = slots, a.end = offsets + groups, a.k = k, a.cols = (int)cols, a.n = tokens * k, a.scales = scales;
     a.past_caches = many(a.n * cols);
     a.dev_status = dev_status;
-    by_type(type, [&](auto t) { launch_gather<t.value, true>(a, tokens, static_cast<hipStream_t>(stream_)); });
+    by_type(type, [&](auto t) {
+        by_pieces(a, tokens, [&](const RowsArgs &b, dim3 grid) {
+            hipLaunchKernelGGL(gather_fp8_kernel<t.value>, grid, dim3(256), 0, static_cast<hipStream_t>(stream_), b);
+        });
+    });
     BK_LAUNCH_CHECK("gather_fp8_kernel");
     return BAKRON_OK;
 }
