@@ -718,9 +718,8 @@ __device__ __forceinline__ void store_any(char *base, int type, int64_t i, int l
 }
 // A workgroup takes a unit's places, 128 columns and 16 RT ranks; its waves share the
 // places, 32 at a time.  A lane reads 8 columns of 8 rows and turns them about with byte
-// permutes: the matrix cores want 8 places of one column.  The waves are as many as a usual
-// unit has turns for (gradients of 4000 rows by 64 groups, 4096 x 4096: 63 us with 2 waves, 84
-// with 8).
+// permutes: the matrix cores want 8 places of one column.  2 or 8 waves (gradients of 4000 rows
+// by 64 groups, 4096 x 4096: 63 us with 2, 84 with 8).
 template <int T, int WAVES, int RT, bool WHOLE>
 __device__ __forceinline__ void outer_sum(const OuterArgs &a, const Outer &job, const Tile &t, int64_t sub, int c0, int r0,
                                           floatx4 (&acc)[8][RT]) {
@@ -929,15 +928,15 @@ Layout layout_of(int64_t rows, int64_t N, int64_t K, int32_t rank, int32_t group
     y.units = groups;
     // Sums over places: a group at a time, or, where that leaves CUs idle and there are places
     // enough to pay for joining, chunks of a group.  A CU holds two workgroups, one of 64 ranks.
-    if (grad) {
-        const int64_t tiles = ((N + 127) / 128 + (K + 127) / 128) * ((blocks + 3) / 4), want = blocks >= 3 ? 256 : 512;
-        if (tiles * groups < want && rows > 2048) {
-            const int64_t splits = (want + tiles - 1) / tiles;
-            y.chunk = (int)std::max<int64_t>(512, round_up((rows + splits - 1) / splits, 128));
-            y.units = row_tiles(y.chunk, rows, groups, true);
-        }
+    const int64_t tiles = ((N + 127) / 128 + (K + 127) / 128) * ((blocks + 3) / 4), want = blocks >= 3 ? 256 : 512;
+    if (grad && tiles * groups < want && rows > 2048) {
+        const int64_t splits = (want + tiles - 1) / tiles;
+        y.chunk = (int)std::max<int64_t>(512, round_up((rows + splits - 1) / splits, 128));
+        y.units = row_tiles(y.chunk, rows, groups, true);
     }
-    y.outer_waves = rows <= 128 * (int64_t)groups ? 2 : 8;
+    // Small groups that are many have work for 2 waves each; where CUs idle, 8 finish sooner (515
+    // rows by 5 groups, 1000 x 520: 8 us, with 2 waves 14).
+    y.outer_waves = rows <= 128 * (int64_t)groups && tiles * groups >= 1024 ? 2 : 8;
     return y;
 }
 
