@@ -164,6 +164,18 @@ def test_gradients(bk, case, dtype, otype):
     close(bk.adapter_matmul_grad(dY, X, A, B, offsets, order, scale, x_dtype=ot, want_w=False)[0], dx, ex)
 
 
+# enough places for workgroups of 64 places by 64 ranks, ragged: of the gradients; of both
+MANY = [(2000, 72, 136, 250, 2, 30, 0, 0), (8200, 131, 72, 48, 4, 100, 3, 1), (17000, 64, 200, 33, 3, 177, 0, 0),
+        (4200, 300, 67, 256, 2, 1, 0, 0)]
+
+
+@pytest.mark.parametrize("case", MANY, ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_many_rows_and_ranks(bk, case, dtype):
+    test_forward(bk, case, dtype, "same")
+    test_gradients(bk, case, dtype, "f32")
+
+
 @pytest.mark.parametrize("rows", [5, 70, 1500])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_one_adapter_without_offsets(bk, rows, dtype):

@@ -201,9 +201,11 @@ constexpr int shrink_lds(int mt, int rt) {
     return shrink_waves(mt, rt) * (through > sums ? through : sums);
 }
 
-// GRAD: matrices of either order.
+// GRAD: matrices of either order.  64 places by 64 ranks take the registers of a whole CU, and read
+// half as much from L2 as 32 by 64 or by twice 32 (gradients, 8192 rows, 4096 x 4096, rank 64:
+// 52 us instead of 67, rank 128: 83 instead of 118).
 template <int T, int MT, int RT, bool GRAD>
-__global__ __launch_bounds__(64 * shrink_waves(MT, RT), 4) void shrink_kernel(ShrinkArgs a) {
+__global__ __launch_bounds__(64 * shrink_waves(MT, RT), MT * RT > 8 ? 2 : 4) void shrink_kernel(ShrinkArgs a) {
     extern __shared__ __align__(16) float space[];
     const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
     constexpr int waves = shrink_waves(MT, RT), KS = SHRINK_STEP, DEPTH = MT * RT == 1 ? 3 : MT * RT == 2 ? 2 : 1;
@@ -896,7 +898,7 @@ __global__ __launch_bounds__(256) void outer_join_kernel(OuterArgs a) {
 // How a call is laid out; the same for workspace and launch.
 struct Layout {
     int mt;                 // 16-place tiles of a tile of expand: 1 or 4
-    int rt;                 // 16-rank blocks of a workgroup of shrink
+    int st, rt;             // 16-place tiles and 16-rank blocks of a workgroup of shrink
     int ranks, rs;          // ranks in whole 16s; 32-rank steps of expand
     int64_t slots;          // tiles of 16 mt places
     int splits;             // of K, in shrink
@@ -905,9 +907,6 @@ struct Layout {
     int outer_waves;        // waves that share a unit's places
 };
 
-// Places that a workgroup of shrink takes, in 16s.
-int shrink_mt(const Layout &y) { return y.mt == 1 ? 1 : 2; }
-
 Layout layout_of(int64_t rows, int64_t N, int64_t K, int32_t rank, int32_t groups, bool grad) {
     Layout y;
     y.ranks = (int)round_up(rank, 16);
@@ -915,9 +914,13 @@ Layout layout_of(int64_t rows, int64_t N, int64_t K, int32_t rank, int32_t group
     y.mt = rows >= 64 * (int64_t)(groups + 1) && rows >= 1024 ? 4 : 1;
     y.slots = row_tiles(16 * y.mt, rows, groups, true);
     const int blocks = y.ranks / 16;
-    // Gradients take 32 ranks at once at most: with 64 and both orders of a matrix the registers
-    // leave one workgroup a CU (8192 rows, rank 128, 4096 x 4096: 250 against 261 us).
+    // Gradients take 32 ranks of 16 or 32 places at most: with 64 and both orders of a matrix the
+    // registers leave one workgroup a CU (8192 rows, rank 128, 4096 x 4096: 250 against 261 us).
     y.rt = y.mt == 1 && y.slots * blocks <= 1024 ? 1 : blocks >= 4 && !grad ? 4 : blocks >= 2 ? 2 : 1;
+    // 64 places by 64 ranks where that makes a workgroup for each CU (8192 rows, rank 64, K = 4096,
+    // 133 of them: 30 us, with 32 places 25).
+    y.st = y.mt == 1 ? 1 : 2;
+    if (y.mt == 4 && blocks >= 3 && y.slots * ((blocks + 3) / 4) * (grad ? 2 : 1) >= 256) y.st = y.rt = 4;
     // Where CUs idle, several workgroups share a tile's K, 2 steps a wave at least (8 rows of
     // their own adapters, rank 16, K = 14336: 10.3 us, unshared 14.9; 64 rows, K = 4096: 10.9 and
     // 11.9).
@@ -946,7 +949,7 @@ template <int T, int MT, int RT>
 void launch_shrink(const ShrinkArgs &a, const Layout &y, int deep, hipStream_t s) {
     const dim3 grid((unsigned)(round_up(y.slots, 8) * (y.mt / MT)), (unsigned)((y.ranks / 16 + RT - 1) / RT), deep);
     const dim3 block(64 * shrink_waves(MT, RT));
-    if constexpr (RT < 4)  // the gradients' layout has no more
+    if constexpr (RT < 4 || MT == 4)  // the gradients' layout has no others
         if (a.job[0].strided) {
             hipLaunchKernelGGL((shrink_kernel<T, MT, RT, true>), grid, block, shrink_lds(MT, RT), s, a);
             return;
@@ -956,7 +959,8 @@ void launch_shrink(const ShrinkArgs &a, const Layout &y, int deep, hipStream_t s
 template <int T>
 void launch_shrink(ShrinkArgs a, const Layout &y, int deep, hipStream_t s) {
     a.high = 16 * y.mt, a.slots = (int)y.slots, a.splits = y.splits, a.part_words = place_words(y);
-    if (shrink_mt(y) == 1) {
+    if (y.st == 4) return launch_shrink<T, 4, 4>(a, y, deep, s);
+    if (y.st == 1) {
         if (y.rt == 1) return launch_shrink<T, 1, 1>(a, y, deep, s);
         if (y.rt == 2) return launch_shrink<T, 1, 2>(a, y, deep, s);
         return launch_shrink<T, 1, 4>(a, y, deep, s);
