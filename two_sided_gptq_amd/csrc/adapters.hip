@@ -88,6 +88,10 @@ __device__ __forceinline__ void split_f16(uintx4 v, uintx4 &hi, uintx4 &lo) {
     }
 }
 
+// What lanes of a wave pass each other through LDS stays in the program's order; the hardware keeps
+// it within a wave, so nothing is waited for.
+__device__ __forceinline__ void order_lanes() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local"); }
+
 // Places of one tile: group g (`groups`: rows of no adapter; -1: nothing) and [p0, p1).
 struct Tile {
     int g, p0, p1, pad;
@@ -298,9 +302,11 @@ __global__ __launch_bounds__(64 * shrink_waves(MT, RT), MT * RT > 8 ? 2 : 4) voi
             const int r = h * PER + lr;
             *reinterpret_cast<uintx4 *>(own + r * (KS * 2) + (lc ^ (r & (CH - 1))) * 16) = v[h];
         }
+        order_lanes();
 #pragma unroll
         for (int h = 0; h < NL; ++h)
             f[h] = *reinterpret_cast<const uintx4 *>(own + l * (KS * 2) + ((h * 4 + q) ^ (l & (CH - 1))) * 16);
+        order_lanes();
     };
     // K x rank: rows of 32 bytes, read with a transposing load: lane l of 16 gets rank l and 4
     // of K from each.
@@ -309,6 +315,7 @@ __global__ __launch_bounds__(64 * shrink_waves(MT, RT), MT * RT > 8 ? 2 : 4) voi
         typedef __attribute__((address_space(3))) shortx4 *lds4;
 #pragma unroll
         for (int h = 0; h < NL; ++h) *reinterpret_cast<uintx4 *>(own + lane * 32 + h * 16) = v[h];
+        order_lanes();
 #pragma unroll
         for (int h = 0; h < NL; ++h) {
             char *at = own + (h * 32 + q * 8 + (l >> 2)) * 32 + (l & 3) * 8;
@@ -317,6 +324,7 @@ __global__ __launch_bounds__(64 * shrink_waves(MT, RT), MT * RT > 8 ? 2 : 4) voi
             __builtin_memcpy(&f[h], &lo, 8);
             __builtin_memcpy(reinterpret_cast<char *>(&f[h]) + 8, &hi, 8);
         }
+        order_lanes();
     };
     // Registers take the loads of step `next` as soon as LDS has what they held.
     auto multiply = [&](uintx4(&gx)[MT][NL], uintx4(&gm)[RT][NL], int next) {
@@ -537,6 +545,7 @@ __device__ __forceinline__ void expand_whole(const ExpandArgs &a, const Tile &t,
                 const int i = k * 64 + lane, r = i * a.per_chunk >> 16;  // i / chunks
                 if (i < some) *reinterpret_cast<uintx4 *>(own + (i + r) * 16) = raw_w[c / PER * WL + k];
             }
+            order_lanes();
 #pragma unroll
             for (int d = 0; d < PER; ++d)
 #pragma unroll
@@ -545,6 +554,7 @@ __device__ __forceinline__ void expand_whole(const ExpandArgs &a, const Tile &t,
                     if (s * 4 + q < chunks)
                         f[c + d][s] = *reinterpret_cast<const uintx4 *>(own + ((d * 16 + l) * (chunks + 1) + s * 4 + q) * 16);
                 }
+            order_lanes();
         }
     } else {
         // rows of 128 bytes, the 32 of 16 columns at place c ^ (row & 3), read with a transposing load
@@ -557,6 +567,7 @@ __device__ __forceinline__ void expand_whole(const ExpandArgs &a, const Tile &t,
                 const int r = k * 8 + lr;
                 *reinterpret_cast<uintx4 *>(own + r * 128 + (((lc >> 1) ^ (r & 3)) * 32) + (lc & 1) * 16) = raw_w[s * 4 + k];
             }
+            order_lanes();
             const int r = q * 8 + (l >> 2);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -566,6 +577,7 @@ __device__ __forceinline__ void expand_whole(const ExpandArgs &a, const Tile &t,
                 __builtin_memcpy(&f[c][s], &lo, 8);
                 __builtin_memcpy(reinterpret_cast<char *>(&f[c][s]) + 8, &hi, 8);
             }
+            order_lanes();
         }
     }
     float *results = reinterpret_cast<float *>(own);
@@ -585,6 +597,7 @@ __device__ __forceinline__ void expand_whole(const ExpandArgs &a, const Tile &t,
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c) *reinterpret_cast<floatx4 *>(results + l * EXPAND_ROW + c * 16 + q * 4) = acc[c];
+            order_lanes();
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -600,6 +613,7 @@ __device__ __forceinline__ void expand_whole(const ExpandArgs &a, const Tile &t,
             }
             if (row[i][h] >= 0) store8<OT>(a.out, row[i][h] * a.ldo + n0 + lc * 8, 8, y);
         }
+        order_lanes();
     }
 }
 
