@@ -506,7 +506,7 @@ __device__ __forceinline__ void store8_past(char *base, int64_t i, const float *
 template <int T, int WAVES, int AT_ONCE>
 __global__ __launch_bounds__(256) void combine_grad_kernel(RowsArgs a) {
     __shared__ float part[4][AT_ONCE];
-    const int lane = lane_id(), w = threadIdx.x >> 6, sub = w % WAVES;
+    const int lane = lane_id(), w = wave_uniform(threadIdx.x >> 6), sub = w % WAVES;
     const int64_t at = (int64_t)blockIdx.x * (4 / WAVES) + w / WAVES;
     const bool mine = at < a.tokens;
     const int64_t token = a.token0 + (mine ? at : 0);
@@ -516,8 +516,14 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(RowsArgs a) {
     for (int j0 = 0; j0 < a.k; j0 += AT_ONCE) {
         float dot[AT_ONCE] = {};
         int slot[AT_ONCE];  // -1: none
+        float weight[AT_ONCE];
+        // here, as lanes leave the loop over columns at different turns
 #pragma unroll
-        for (int j = 0; j < AT_ONCE; ++j) slot[j] = mine && j0 + j < a.k ? from_lane(slots, j0 + j) : -1;
+        for (int j = 0; j < AT_ONCE; ++j) {
+            const bool some = mine && j0 + j < a.k;
+            slot[j] = some ? from_lane(slots, j0 + j) : -1;
+            weight[j] = some ? from_lane(weights, j0 + j) : 0.0f;
+        }
         // what a turn reads is asked for in the turn before
         Raw8<T> d, r[AT_ONCE];
         auto load = [&](int col) {
@@ -543,13 +549,12 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(RowsArgs a) {
                 if (slot[j] < 0) continue;
                 float dy[8] = {};
                 if (slot[j] < end) {
-                    const float weight = from_lane(weights, (j0 + j) & 63);
                     float y[8];
                     unpack8<T>(now[j].w, y);
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         dot[j] += x[q] * y[q];
-                        dy[q] = weight * x[q];
+                        dy[q] = weight[j] * x[q];
                     }
                 }
                 if (past && left >= 8)
