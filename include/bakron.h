@@ -477,9 +477,10 @@ int32_t bakron_group_combine_grad(const void *dout, int64_t ldd, const void *Y, 
  *   base, out  rows x N of that type or fp32 (`otype`); base NULL counts as 0, and base
  *      may be out: then rows without adapter are left as they are
  *   ws  *_workspace_size() bytes
- * Sums are in fp32.  The rank values between the two products keep 16 bits (a relative
- * 2^-16), out is rounded once.  What depends on a value that is not finite is not finite
- * (where the formula has an infinity it may be a NaN).
+ * Sums are in fp32.  The rank values between the two products keep fp32's 24 bits where
+ * the result is fp32, and 16 (a relative 2^-16) where it is of 16 bits; the result is
+ * rounded once.  What depends on a value that is not finite is not finite (where the
+ * formula has an infinity it may be a NaN).
  *
  * bakron_adapter_matmul_grad -- for dY (rows x N), with U = scale dY B and
  * P = scale X A^T:

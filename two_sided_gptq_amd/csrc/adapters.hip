@@ -10,9 +10,12 @@
 //
 // shrink_kernel makes P (or U): a workgroup takes a tile of 16 MT places of one group, its
 // waves share K.  expand_kernel adds P B^T to the base, a wave 64 columns at a time.
-// outer_kernel sums over a group's places.  In between P and U are kept as two bf16 numbers
-// each, x = hi + lo (2^-16 |x| is lost): the products with both parts are exact in
-// fp32 sums, and neither fp16's range nor bf16's 8 bits limit what lies between two products.
+// outer_kernel sums over a group's places.  In between P and U are kept in 32 bits, and go into
+// the matrix cores as a sum of bf16 numbers, so that neither fp16's range nor bf16's 8 bits limit
+// what lies between two products.  For results in 16 bits they are two numbers, hi + lo: what
+// that loses, 2^-16 of a value, is far below half a step of the result (2^-11 in fp16).  For
+// results in fp32 they are fp32 numbers, which three bf16 parts of 8 bits hold exactly.  The
+// products of every part are exact in fp32 sums.
 #include <algorithm>
 
 #include "common.hpp"
@@ -68,12 +71,31 @@ __device__ __forceinline__ uint32_t pack_parts(float x) {
     const uint32_t lo = __builtin_isfinite(h) ? f32_to_bf16(x - h) : 0;
     return hi << 16 | lo;
 }
-// 8 packed numbers as the two operands' fragments.
-__device__ __forceinline__ void unpack_parts(const uint32_t *x, uintx4 &hi, uintx4 &lo) {
+// Parts of the numbers between the products, by the type of the result.
+constexpr int parts_of(int otype) { return otype == BAKRON_T_F32 ? 3 : 2; }
+template <int PARTS>
+__device__ __forceinline__ uint32_t pack(float x) {
+    return PARTS == 2 ? pack_parts(x) : __float_as_uint(x);
+}
+__device__ __forceinline__ uint32_t pack(float x, int parts) { return parts == 2 ? pack<2>(x) : pack<3>(x); }
+// 8 packed numbers as the operands' fragments, one of each part.  Three: an fp32 number's upper
+// 8 bits, those of what that leaves, and the rest, which has 8 at most.
+template <int PARTS>
+__device__ __forceinline__ void unpack_parts(const uint32_t *x, uintx4 (&part)[PARTS]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        hi[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], 0x07060302);
-        lo[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], 0x05040100);
+        uint32_t a = x[2 * j], b = x[2 * j + 1];
+        if constexpr (PARTS == 2) {
+            part[0][j] = __builtin_amdgcn_perm(b, a, 0x07060302);
+            part[1][j] = __builtin_amdgcn_perm(b, a, 0x05040100);
+        } else {
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+                part[p][j] = __builtin_amdgcn_perm(b, a, 0x07060302);
+                a = __float_as_uint(__uint_as_float(a) - __uint_as_float(a & 0xffff0000u));
+                b = __float_as_uint(__uint_as_float(b) - __uint_as_float(b & 0xffff0000u));
+            }
+        }
     }
 }
 // 8 fp16 values as bf16 parts, exactly: 11 bits are 8 and what is left.
@@ -184,6 +206,7 @@ struct Shrink {
     int K, strided;         // the matrix is rank x K (0) or K x rank (1)
     uint32_t *by_place;     // [16-place tile][16][ranks], or NULL
     uint32_t *by_rank;      // [16-place tile][ranks][16], or NULL
+    int place_parts, rank_parts;  // what they are packed as
 };
 struct ShrinkArgs {
     Groups of;
@@ -389,17 +412,23 @@ __global__ __launch_bounds__(64 * shrink_waves(MT, RT), MT * RT > 8 ? 2 : 4) voi
             // lane: rank l, places 4 q ..
             const int64_t tile = (int64_t)slot * (a.high / 16) + sub + i;
             const int rank = r0 + j * 16 + l;
-            uintx4 packed;
+            float x[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const bool ok = __shfl(row[i], q * 4 + e) >= 0 && rank < a.rank;
-                const float x = ok ? s[e] * scale : 0.0f;
-                packed[e] = splits > 1 ? __float_as_uint(x) : pack_parts(x);
+                x[e] = ok ? s[e] * scale : 0.0f;
             }
-            if (job.by_rank) *reinterpret_cast<uintx4 *>(job.by_rank + (tile * a.ranks + rank) * 16 + q * 4) = packed;
+            if (job.by_rank) {
+                uintx4 packed;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) packed[e] = pack(x[e], job.rank_parts);
+                *reinterpret_cast<uintx4 *>(job.by_rank + (tile * a.ranks + rank) * 16 + q * 4) = packed;
+            }
             if (job.by_place)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) job.by_place[part * a.part_words + (tile * 16 + q * 4 + e) * a.ranks + rank] = packed[e];
+                for (int e = 0; e < 4; ++e)
+                    job.by_place[part * a.part_words + (tile * 16 + q * 4 + e) * a.ranks + rank] =
+                        splits > 1 ? __float_as_uint(x[e]) : pack(x[e], job.place_parts);
         }
 }
 
@@ -429,21 +458,24 @@ struct ExpandArgs {
 // shrink_kernel), and passes through LDS of the wave's own to and from the lanes that the
 // matrix cores want it in.  All loads are on their way before the first is waited for.
 // Needs 256 columns and, where W is N x rank, ranks in whole 8s.
-template <int T>
-__device__ __forceinline__ void add_products(const uintx4 &f, const uintx4 &hi, const uintx4 &lo, floatx4 &acc) {
+template <int T, int PARTS>
+__device__ __forceinline__ void add_products(const uintx4 &f, const uintx4 (&part)[PARTS], floatx4 &acc) {
     if constexpr (T == BAKRON_T_BF16) {
-        acc = mfma_bf16(f, lo, mfma_bf16(f, hi, acc));
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) acc = mfma_bf16(f, part[p], acc);
     } else {
         uintx4 fh, fl;
         split_f16(f, fh, fl);
-        acc = mfma_bf16(fh, lo, mfma_bf16(fh, hi, acc));
-        acc = mfma_bf16(fl, lo, mfma_bf16(fl, hi, acc));
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) acc = mfma_bf16(fh, part[p], acc);
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) acc = mfma_bf16(fl, part[p], acc);
     }
 }
 
 // P of the tile's places, on its way from memory, 16 bytes a thread and turn; then to LDS,
 // rows of `ranks` 4 words apart.
-template <int MT, int RS>
+template <int MT, int RS, int PARTS>
 struct StagedP {
     static constexpr int TURNS = (MT * RS + 1) / 2;
     uintx4 v[TURNS];
@@ -463,7 +495,7 @@ struct StagedP {
 #pragma unroll 1
             for (int m = 1; m < a.splits; ++m) sum += *reinterpret_cast<const floatx4 *>(p + m * a.part_words + i);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[k][e] = pack_parts(sum[e]);
+            for (int e = 0; e < 4; ++e) v[k][e] = pack<PARTS>(sum[e]);
         }
     }
     __device__ __forceinline__ void store(const ExpandArgs &a, int words, uint32_t *lds) const {
@@ -475,24 +507,25 @@ struct StagedP {
     }
 };
 
-__device__ __forceinline__ void p_frags(const ExpandArgs &a, const uint32_t *lds, int place, int r, uintx4 &hi, uintx4 &lo) {
+template <int PARTS>
+__device__ __forceinline__ void p_frags(const ExpandArgs &a, const uint32_t *lds, int place, int r, uintx4 (&part)[PARTS]) {
     uint32_t p[8] = {};
     if (r < a.ranks) __builtin_memcpy(p, __builtin_assume_aligned(lds + place * (a.ranks + 4) + r, 16), 32);
-    unpack_parts(p, hi, lo);
+    unpack_parts(p, part);
 }
 
 constexpr int EXPAND_ROW = 68;  // floats between the rows of results in LDS
 
 template <int T, int OT, int MT, int RS, bool STRIDED>
 __device__ __forceinline__ void expand_whole(const ExpandArgs &a, const Tile &t, int64_t slot, int n0, uint32_t *lds, char *own) {
-    constexpr int OS = OT == BAKRON_T_F32 ? 4 : 2;
+    constexpr int OS = OT == BAKRON_T_F32 ? 4 : 2, PARTS = parts_of(OT);
     constexpr int PER = RS == 1 ? 4 : 1;          // 16-row pieces of W that pass at a time
     constexpr int WL = RS == 1 ? 4 : 2 * RS / 2;  // loads of a pass
     const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4, lr = lane >> 3, lc = lane & 7;
     const bool none = t.g == a.of.groups;
     const int count = t.p1 - t.p0;
     const int words = none ? 0 : (count + 15) / 16 * 16 * a.ranks;
-    StagedP<MT, RS> p;
+    StagedP<MT, RS, PARTS> p;
     p.load(a, slot, words);
     int row[MT][2];
 #pragma unroll
@@ -590,10 +623,10 @@ __device__ __forceinline__ void expand_whole(const ExpandArgs &a, const Tile &t,
         if (!none) {
 #pragma unroll
             for (int s = 0; s < RS; ++s) {
-                uintx4 hi, lo;
-                p_frags(a, lds, i * 16 + l, s * 32 + q * 8, hi, lo);
+                uintx4 part[PARTS];
+                p_frags(a, lds, i * 16 + l, s * 32 + q * 8, part);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) add_products<T>(f[c][s], hi, lo, acc[c]);
+                for (int c = 0; c < 4; ++c) add_products<T>(f[c][s], part, acc[c]);
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c) *reinterpret_cast<floatx4 *>(results + l * EXPAND_ROW + c * 16 + q * 4) = acc[c];
@@ -622,6 +655,7 @@ __device__ __forceinline__ void expand_whole(const ExpandArgs &a, const Tile &t,
 // c is column 32 (c / 2) + 8 (m / 4) + 4 (c % 2) + m % 4.
 template <int T, int OT, int MT, int RS, bool STRIDED>
 __device__ __forceinline__ void expand_any(const ExpandArgs &a, const Tile &t, int64_t slot, int n0, uint32_t *lds) {
+    constexpr int PARTS = parts_of(OT);
     const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
     const bool none = t.g == a.of.groups;
     const int count = t.p1 - t.p0, col = n0 + q * 8, left = a.N - col;
@@ -644,7 +678,7 @@ __device__ __forceinline__ void expand_any(const ExpandArgs &a, const Tile &t, i
             }
         }
     }
-    StagedP<MT, RS> p;
+    StagedP<MT, RS, PARTS> p;
     const int words = none ? 0 : (count + 15) / 16 * 16 * a.ranks;
     p.load(a, slot, words);
     p.store(a, words, lds);
@@ -661,10 +695,10 @@ __device__ __forceinline__ void expand_any(const ExpandArgs &a, const Tile &t, i
             for (int c = 0; c < 4; ++c) acc[c] = floatx4{0, 0, 0, 0};
 #pragma unroll
             for (int s = 0; s < RS; ++s) {
-                uintx4 hi, lo;
-                p_frags(a, lds, i * 16 + l, s * 32 + q * 8, hi, lo);
+                uintx4 part[PARTS];
+                p_frags(a, lds, i * 16 + l, s * 32 + q * 8, part);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) add_products<T>(f[c][s], hi, lo, acc[c]);
+                for (int c = 0; c < 4; ++c) add_products<T>(f[c][s], part, acc[c]);
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -736,7 +770,7 @@ __device__ __forceinline__ void store_any(char *base, int type, int64_t i, int l
 // places, 32 at a time.  A lane reads 8 columns of 8 rows and turns them about with byte
 // permutes: the matrix cores want 8 places of one column.  2 or 8 waves (gradients of 4000 rows
 // by 64 groups, 4096 x 4096: 63 us with 2, 84 with 8).
-template <int T, int WAVES, int RT, bool WHOLE>
+template <int T, int WAVES, int RT, int PARTS, bool WHOLE>
 __device__ __forceinline__ void outer_sum(const OuterArgs &a, const Outer &job, const Tile &t, int64_t sub, int c0, int r0,
                                           floatx4 (&acc)[8][RT]) {
     const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
@@ -774,9 +808,9 @@ __device__ __forceinline__ void outer_sum(const OuterArgs &a, const Outer &job, 
             for (int e = 0; e < 8; ++e)
                 if (__shfl(row, q * 8 + e) < 0) v[e] = uintx4{0, 0, 0, 0};
         }
-        uintx4 gh[RT], gl[RT];
+        uintx4 part[RT][PARTS];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) unpack_parts(g[r], gh[r], gl[r]);
+        for (int r = 0; r < RT; ++r) unpack_parts(g[r], part[r]);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             uintx4 f;
@@ -784,12 +818,12 @@ __device__ __forceinline__ void outer_sum(const OuterArgs &a, const Outer &job, 
             for (int j = 0; j < 4; ++j)
                 f[j] = __builtin_amdgcn_perm(v[2 * j + 1][c / 2], v[2 * j][c / 2], c & 1 ? 0x07060302 : 0x05040100);
 #pragma unroll
-            for (int r = 0; r < RT; ++r) add_products<T>(f, gh[r], gl[r], acc[c][r]);
+            for (int r = 0; r < RT; ++r) add_products<T>(f, part[r], acc[c][r]);
         }
     }
 }
 
-template <int T, int WAVES, int RT>
+template <int T, int WAVES, int RT, int PARTS>
 __global__ __launch_bounds__(64 * WAVES) void outer_kernel(OuterArgs a) {
     // half of the waves' sums; then the results as rows of the output
     constexpr int HALF = WAVES / 2 * 8 * RT * 256, BY_RANK = 128 + 4, BY_COLUMN = 16 * RT + 4;
@@ -829,9 +863,9 @@ __global__ __launch_bounds__(64 * WAVES) void outer_kernel(OuterArgs a) {
 #pragma unroll
         for (int r = 0; r < RT; ++r) acc[c][r] = floatx4{0, 0, 0, 0};
     if (c0 + 128 <= job.cols)
-        outer_sum<T, WAVES, RT, true>(a, job, t, sub, c0, r0, acc);
+        outer_sum<T, WAVES, RT, PARTS, true>(a, job, t, sub, c0, r0, acc);
     else
-        outer_sum<T, WAVES, RT, false>(a, job, t, sub, c0, r0, acc);
+        outer_sum<T, WAVES, RT, PARTS, false>(a, job, t, sub, c0, r0, acc);
     // the upper half of the waves to the lower, until one is left
 #pragma unroll
     for (int half = WAVES / 2; half > 0; half >>= 1) {
@@ -1005,21 +1039,24 @@ void launch_expand(const ExpandArgs &a, int32_t otype, const Layout &y, hipStrea
         y.mt == 1 ? launch_expand<T, T, 1, STRIDED>(a, y, s) : launch_expand<T, T, 4, STRIDED>(a, y, s);
 }
 
-template <int T, int WAVES>
+template <int T, int WAVES, int PARTS>
 void launch_outer(const OuterArgs &a, const Layout &y, hipStream_t s) {
     const int64_t across = (std::max(a.job[0].cols, a.job[1].cols) + 127) / 128;
     const int blocks = y.ranks / 16;
     const unsigned x = (unsigned)(across * a.units);
     if (blocks == 1)
-        hipLaunchKernelGGL((outer_kernel<T, WAVES, 1>), dim3(x, 1, 2), dim3(64 * WAVES), 0, s, a);
+        hipLaunchKernelGGL((outer_kernel<T, WAVES, 1, PARTS>), dim3(x, 1, 2), dim3(64 * WAVES), 0, s, a);
     else if (blocks == 2)
-        hipLaunchKernelGGL((outer_kernel<T, WAVES, 2>), dim3(x, 1, 2), dim3(64 * WAVES), 0, s, a);
+        hipLaunchKernelGGL((outer_kernel<T, WAVES, 2, PARTS>), dim3(x, 1, 2), dim3(64 * WAVES), 0, s, a);
     else
-        hipLaunchKernelGGL((outer_kernel<T, WAVES, 4>), dim3(x, (unsigned)((blocks + 3) / 4), 2), dim3(64 * WAVES), 0, s, a);
+        hipLaunchKernelGGL((outer_kernel<T, WAVES, 4, PARTS>), dim3(x, (unsigned)((blocks + 3) / 4), 2), dim3(64 * WAVES), 0, s, a);
 }
 template <int T>
 void launch_outer(const OuterArgs &a, const Layout &y, hipStream_t s) {
-    y.outer_waves == 2 ? launch_outer<T, 2>(a, y, s) : launch_outer<T, 8>(a, y, s);
+    if (parts_of(a.otype) == 3)
+        y.outer_waves == 2 ? launch_outer<T, 2, 3>(a, y, s) : launch_outer<T, 8, 3>(a, y, s);
+    else
+        y.outer_waves == 2 ? launch_outer<T, 2, 2>(a, y, s) : launch_outer<T, 8, 2>(a, y, s);
     if (a.chunk) {
         const int64_t threads = (a.rank * (int64_t)std::max(a.job[0].cols, a.job[1].cols) + 7) / 8;
         hipLaunchKernelGGL(outer_join_kernel, dim3((unsigned)((threads + 255) / 256), a.of.groups, 2), dim3(256), 0, s, a);
@@ -1127,7 +1164,7 @@ extern "C" int32_t bakron_adapter_matmul(const void *X, int32_t type, int64_t ld
     uint32_t *p = c.take<uint32_t>(y.splits * place_words(y));
     ShrinkArgs h = {};
     h.of = of, h.scale = scale, h.rank = rank, h.ranks = y.ranks, h.tiles = tiles, h.rows = place_rows;
-    h.job[0] = {static_cast<const char *>(X), static_cast<const char *>(A), ldx, rank * K, (int)K, 0, p, nullptr};
+    h.job[0] = {static_cast<const char *>(X), static_cast<const char *>(A), ldx, rank * K, (int)K, 0, p, nullptr, parts_of(otype), 0};
     ExpandArgs e = {};
     e.of = of, e.tiles = tiles, e.rows = place_rows, e.splits = y.splits, e.part_words = place_words(y), e.p = p, e.w = static_cast<const char *>(B), e.group_w = N * rank;
     e.base = static_cast<const char *>(base), e.out = static_cast<char *>(out), e.ldb = ldb, e.ldo = ldo;
@@ -1192,8 +1229,8 @@ extern "C" int32_t bakron_adapter_matmul_grad(const void *dY, int64_t lddy, cons
 
     ShrinkArgs h = {};
     h.of = of, h.scale = scale, h.rank = rank, h.ranks = y.ranks, h.tiles = tiles, h.rows = place_rows;
-    h.job[0] = {dy, b, lddy, N * rank, (int)N, 1, u, ur};
-    h.job[1] = {x, a, ldx, rank * K, (int)K, 0, nullptr, pr};
+    h.job[0] = {dy, b, lddy, N * rank, (int)N, 1, u, ur, parts_of(xtype), parts_of(wtype)};
+    h.job[1] = {x, a, ldx, rank * K, (int)K, 0, nullptr, pr, 0, parts_of(wtype)};
     const int jobs = dA ? 2 : 1;
     type == BAKRON_T_BF16 ? launch_shrink<BAKRON_T_BF16>(h, y, jobs, s) : launch_shrink<BAKRON_T_F16>(h, y, jobs, s);
 
