@@ -127,3 +127,26 @@ def test_results_of_both_types(bk, dtype):
     assert torch.equal(x, narrow[0]) and torch.equal(a.cpu().double(), dA) and torch.equal(b.cpu().double(), dB)
     x, a, b = bk.adapter_matmul_grad(*args, base=c.base[256].cuda())
     assert torch.equal(x.cpu().double(), dX) and torch.equal(a, narrow[1]) and torch.equal(b, narrow[2])
+
+
+@pytest.mark.parametrize("rows", [4, 1100])
+@pytest.mark.parametrize("dtype,out_dtype", [("bf16", torch.bfloat16), ("bf16", torch.float32), ("f16", torch.float32)])
+def test_values_of_p_and_u_just_below_the_largest(bk, rows, dtype, out_dtype):
+    """P and U are 2^128 - 2^119, whose 9 bits bf16 would round to infinity.  The other matrix brings them
+    back to 2^28 - 2^19 (2^114 - 2^105 from fp16): fp32 holds that, and bf16's nearest, a tie, is 2^28."""
+    t, N, rank = DT[dtype], 300, 2
+    # 2^64 (2^63 + .. + 2^55); from fp16 2^14 (2^13 + .. + 2^5) 2^100
+    one, high, scale, back = (2.0 ** 64, 63, 1.0, 2.0 ** -100) if dtype == "bf16" else (2.0 ** 14, 13, 2.0 ** 100, 2.0 ** -14)
+    powers = torch.zeros(N, dtype=torch.float64)
+    powers[:9] = 2.0 ** (high - torch.arange(9, dtype=torch.float64))
+    A, B = powers.expand(1, rank, N).to(t).cuda(), torch.zeros(1, N, rank, dtype=t, device="cuda")
+    B[0, 5, 1] = back
+    X = torch.full((rows, N), one, dtype=t, device="cuda")
+    s = torch.full((1,), scale, device="cuda")
+    want = torch.zeros(rows, N)
+    want[:, 5] = (2.0 ** 128 - 2.0 ** 119) * back
+    assert torch.equal(bk.adapter_matmul(X, A, B, scale=s, out_dtype=out_dtype).cpu(), want.to(out_dtype))
+    # U: X in dY's place, A in that of B and B in that of A
+    dX = bk.adapter_matmul_grad(X, X, B.transpose(1, 2).contiguous(), A.transpose(1, 2).contiguous(), scale=s,
+                                x_dtype=out_dtype, want_w=False)[0]
+    assert torch.equal(dX.cpu(), want.to(out_dtype))

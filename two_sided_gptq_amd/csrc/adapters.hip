@@ -66,7 +66,8 @@ __device__ __forceinline__ uintx4 load_whole(const char *base, int64_t i) {
 
 // x as two bf16 numbers, hi in the upper half.
 __device__ __forceinline__ uint32_t pack_parts(float x) {
-    const uint32_t hi = f32_to_bf16(x);
+    uint32_t hi = f32_to_bf16(x);
+    if ((hi & 0x7fff) == 0x7f80) hi = __float_as_uint(x) >> 16;  // rounded up to infinity: the largest below
     const float h = __uint_as_float(hi << 16);
     const uint32_t lo = __builtin_isfinite(h) ? f32_to_bf16(x - h) : 0;
     return hi << 16 | lo;
@@ -77,7 +78,6 @@ template <int PARTS>
 __device__ __forceinline__ uint32_t pack(float x) {
     return PARTS == 2 ? pack_parts(x) : __float_as_uint(x);
 }
-__device__ __forceinline__ uint32_t pack(float x, int parts) { return parts == 2 ? pack<2>(x) : pack<3>(x); }
 // 8 packed numbers as the operands' fragments, one of each part.  Three: an fp32 number's upper
 // 8 bits, those of what that leaves, and the rest, which has 8 at most.
 template <int PARTS>
@@ -412,23 +412,20 @@ __global__ __launch_bounds__(64 * shrink_waves(MT, RT), MT * RT > 8 ? 2 : 4) voi
             // lane: rank l, places 4 q ..
             const int64_t tile = (int64_t)slot * (a.high / 16) + sub + i;
             const int rank = r0 + j * 16 + l;
-            float x[4];
+            uintx4 whole, packed;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const bool ok = __shfl(row[i], q * 4 + e) >= 0 && rank < a.rank;
-                x[e] = ok ? s[e] * scale : 0.0f;
+                const float x = ok ? s[e] * scale : 0.0f;
+                whole[e] = pack<3>(x), packed[e] = pack<2>(x);
             }
-            if (job.by_rank) {
-                uintx4 packed;
+            if (job.by_rank)
+                *reinterpret_cast<uintx4 *>(job.by_rank + (tile * a.ranks + rank) * 16 + q * 4) = job.rank_parts == 2 ? packed : whole;
+            if (job.by_place) {
+                const uintx4 v = job.place_parts == 2 && splits == 1 ? packed : whole;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) packed[e] = pack(x[e], job.rank_parts);
-                *reinterpret_cast<uintx4 *>(job.by_rank + (tile * a.ranks + rank) * 16 + q * 4) = packed;
+                for (int e = 0; e < 4; ++e) job.by_place[part * a.part_words + (tile * 16 + q * 4 + e) * a.ranks + rank] = v[e];
             }
-            if (job.by_place)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    job.by_place[part * a.part_words + (tile * 16 + q * 4 + e) * a.ranks + rank] =
-                        splits > 1 ? __float_as_uint(x[e]) : pack(x[e], job.place_parts);
         }
 }
 
