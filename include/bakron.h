@@ -472,7 +472,9 @@ int32_t bakron_group_combine_grad(const void *dout, int64_t ldd, const void *Y, 
  * bakron_adapter_matmul -- out[r] = base[r] + scale_g B_g (A_g X[r]) for row r of adapter
  * g, base[r] for a row without one
  *   X  rows x K;  A  groups x rank x K;  B  groups x N x rank (A and B contiguous): bf16 or
- *      fp16 (`type`).  rank 1 .. 256.
+ *      fp16 (`type`).  rank 1 .. 256; rows, N and K up to 2^24, where tiles of 16 rows by 256
+ *      columns (64 rows, of large batches) fit a launch: (rows / 16 + groups) max(N, K) below
+ *      about 2^32, in the gradients also 4 groups max(N, K).
  *   scale  groups fp32, or NULL for 1
  *   base, out  rows x N of that type or fp32 (`otype`); base NULL counts as 0, and base
  *      may be out: then rows without adapter are left as they are

@@ -1062,27 +1062,24 @@ void launch_outer(const OuterArgs &a, const Layout &y, hipStream_t s) {
 
 bool aligned(const void *p, int64_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
-bool sizes_ok(int64_t rows, int64_t N, int64_t K, int32_t rank, int32_t groups) {
+bool sizes_ok(int64_t rows, int64_t N, int64_t K, int32_t rank, int32_t groups, bool grad) {
     if (!(rows >= 1 && N >= 1 && K >= 1 && rows <= MAX_DIM && N <= MAX_DIM && K <= MAX_DIM && rank >= 1 &&
           rank <= MAX_RANK && groups >= 1 && groups <= MAX_GROUPS))
         return false;
     // no launch of 2^32 threads or more in a dimension; expand and outer are the widest
     const int64_t most = std::max(N, K);
-    for (bool grad : {false, true}) {
-        const Layout y = layout_of(rows, N, K, rank, groups, grad);
-        if (y.slots * ((most + 255) / 256) * 256 > LAUNCH_THREADS) return false;
-        if (grad && y.units * ((most + 127) / 128) * 64 * y.outer_waves > LAUNCH_THREADS) return false;
-    }
-    return true;
+    const Layout y = layout_of(rows, N, K, rank, groups, grad);
+    return y.slots * ((most + 255) / 256) * 256 <= LAUNCH_THREADS &&
+           (!grad || y.units * ((most + 127) / 128) * 64 * y.outer_waves <= LAUNCH_THREADS);
 }
 
 int32_t check_common(int64_t rows, int64_t N, int64_t K, int32_t rank, int32_t groups, const int32_t *offsets,
-                     int32_t type) {
+                     int32_t type, bool grad) {
     BK_REQUIRE(rows >= 1 && N >= 1 && K >= 1 && rows <= MAX_DIM && N <= MAX_DIM && K <= MAX_DIM,
                "bad sizes rows=%lld N=%lld K=%lld", (long long)rows, (long long)N, (long long)K);
     BK_REQUIRE(rank >= 1 && rank <= MAX_RANK, "rank must be in 1 .. %d, not %d", MAX_RANK, rank);
     BK_REQUIRE(groups >= 1 && groups <= MAX_GROUPS, "groups must be in 1 .. %d, not %d", MAX_GROUPS, groups);
-    BK_REQUIRE(sizes_ok(rows, N, K, rank, groups), "too many tiles: rows=%lld N=%lld K=%lld groups=%d", (long long)rows,
+    BK_REQUIRE(sizes_ok(rows, N, K, rank, groups, grad), "too many tiles: rows=%lld N=%lld K=%lld groups=%d", (long long)rows,
                (long long)N, (long long)K, groups);
     BK_REQUIRE(offsets || groups == 1, "offsets must be non-NULL for %d groups", groups);
     BK_REQUIRE(type == BAKRON_T_BF16 || type == BAKRON_T_F16, "type must be bf16 or fp16, not %d", type);
@@ -1130,7 +1127,7 @@ using namespace bakron;
 
 extern "C" size_t bakron_adapter_matmul_workspace_size(int64_t rows, int64_t N, int64_t K, int32_t rank,
                                                        int32_t groups) {
-    if (!sizes_ok(rows, N, K, rank, groups)) return 0;
+    if (!sizes_ok(rows, N, K, rank, groups, false)) return 0;
     const Layout y = layout_of(rows, N, K, rank, groups, false);
     return tiles_size(y) + align256(y.splits * place_words(y) * 4);
 }
@@ -1142,7 +1139,7 @@ extern "C" int32_t bakron_adapter_matmul(const void *X, int32_t type, int64_t ld
                                          int32_t *dev_status, void *ws, size_t ws_bytes, void *stream_) {
     clear_error();
     BK_REQUIRE(X && A && B && out, "X, A, B and out must be non-NULL");
-    BK_TRY(check_common(rows, N, K, rank, groups, offsets, type));
+    BK_TRY(check_common(rows, N, K, rank, groups, offsets, type, false));
     BK_TRY(check_ld("ldx", ldx, K));
     BK_TRY(check_ld("ldo", ldo, N));
     if (base) BK_TRY(check_ld("ldb", ldb, N));
@@ -1179,7 +1176,7 @@ extern "C" int32_t bakron_adapter_matmul(const void *X, int32_t type, int64_t ld
 
 extern "C" size_t bakron_adapter_matmul_grad_workspace_size(int64_t rows, int64_t N, int64_t K, int32_t rank,
                                                             int32_t groups) {
-    if (!sizes_ok(rows, N, K, rank, groups)) return 0;
+    if (!sizes_ok(rows, N, K, rank, groups, true)) return 0;
     return grad_size(layout_of(rows, N, K, rank, groups, true), N, K, rank, true, true);
 }
 
@@ -1194,7 +1191,7 @@ extern "C" int32_t bakron_adapter_matmul_grad(const void *dY, int64_t lddy, cons
     BK_REQUIRE(dX || (dA && dB), "dX, or dA and dB, must be non-NULL");
     BK_REQUIRE(!dA == !dB, "dA and dB go together");
     BK_REQUIRE(X || !dA, "dA and dB need X");
-    BK_TRY(check_common(rows, N, K, rank, groups, offsets, type));
+    BK_TRY(check_common(rows, N, K, rank, groups, offsets, type, true));
     BK_TRY(check_ld("lddy", lddy, N));
     if (dA) BK_TRY(check_ld("ldx", ldx, K));
     if (dX) {
