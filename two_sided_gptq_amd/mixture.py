@@ -111,6 +111,10 @@ def main():
     p.add_argument("--requests", type=int, default=16)
     p.add_argument("--bits", type=int, default=4, choices=(2, 3, 4))
     a = p.parse_args()
+    if not 1 <= a.choices <= a.experts:
+        p.error(f"a token cannot choose {a.choices} of {a.experts} experts")
+    if a.requests < 1 or a.tokens % a.requests or a.tokens < 2 * a.requests:
+        p.error(f"{a.tokens} tokens are not two or more for each of {a.requests} requests, of the same number")
     X, gate, W, W8, scales, adapters = example(a.experts, a.choices, a.tokens, a.width, a.requests, bits=a.bits)
     experts, weights = route(X, gate, a.choices)
     rounded = forward(X, experts, weights, W8, scales, adapters)
