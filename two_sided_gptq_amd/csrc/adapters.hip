@@ -230,7 +230,8 @@ constexpr int shrink_lds(int mt, int rt) {
 
 // GRAD: matrices of either order.  64 places by 64 ranks take the registers of a whole CU, and read
 // half as much from L2 as 32 by 64 or by twice 32 (gradients, 8192 rows, 4096 x 4096, rank 64:
-// 52 us instead of 67, rank 128: 83 instead of 118).
+// 52 us instead of 67, rank 128: 83 instead of 118).  Of the others, 32 places by 64 ranks needs 3
+// registers more than 4 waves a SIMD leave, and puts them aside in scratch memory.
 template <int T, int MT, int RT, bool GRAD>
 __global__ __launch_bounds__(64 * shrink_waves(MT, RT), MT * RT > 8 ? 2 : 4) void shrink_kernel(ShrinkArgs a) {
     extern __shared__ __align__(16) float space[];
@@ -447,14 +448,7 @@ struct ExpandArgs {
     int per_chunk;          // 2^16 / (rank / 8), rounded up: divides what is below 2^11
 };
 
-// D = W P^T with W's rows as the first operand: a lane then holds 4 of W's rows (columns of
-// out) for one place.  A workgroup takes a tile's places and 256 columns, a wave 64 of
-// them: W's part stays in registers, P in LDS.
-//
-// All that is in memory is read and written along rows by neighbouring lanes (see
-// shrink_kernel), and passes through LDS of the wave's own to and from the lanes that the
-// matrix cores want it in.  All loads are on their way before the first is waited for.
-// Needs 256 columns and, where W is N x rank, ranks in whole 8s.
+// The products of a matrix's fragment with every part of P's or U's.
 template <int T, int PARTS>
 __device__ __forceinline__ void add_products(const uintx4 &f, const uintx4 (&part)[PARTS], floatx4 &acc) {
     if constexpr (T == BAKRON_T_BF16) {
@@ -513,6 +507,14 @@ __device__ __forceinline__ void p_frags(const ExpandArgs &a, const uint32_t *lds
 
 constexpr int EXPAND_ROW = 68;  // floats between the rows of results in LDS
 
+// D = W P^T with W's rows as the first operand: a lane then holds 4 of W's rows (columns of
+// out) for one place.  A workgroup takes a tile's places and 256 columns, a wave 64 of
+// them: W's part stays in registers, P in LDS.
+//
+// All that is in memory is read and written along rows by neighbouring lanes (see
+// shrink_kernel), and passes through LDS of the wave's own to and from the lanes that the
+// matrix cores want it in.  All loads are on their way before the first is waited for.
+// Needs 256 columns and, where W is N x rank, ranks in whole 8s.
 template <int T, int OT, int MT, int RS, bool STRIDED>
 __device__ __forceinline__ void expand_whole(const ExpandArgs &a, const Tile &t, int64_t slot, int n0, uint32_t *lds, char *own) {
     constexpr int OS = OT == BAKRON_T_F32 ? 4 : 2, PARTS = parts_of(OT);
@@ -959,8 +961,9 @@ Layout layout_of(int64_t rows, int64_t N, int64_t K, int32_t rank, int32_t group
     y.mt = rows >= 64 * (int64_t)(groups + 1) && rows >= 1024 ? 4 : 1;
     y.slots = row_tiles(16 * y.mt, rows, groups, true);
     const int blocks = y.ranks / 16;
-    // Gradients take 32 ranks of 16 or 32 places at most: with 64 and both orders of a matrix the
-    // registers leave one workgroup a CU (8192 rows, rank 128, 4096 x 4096: 250 against 261 us).
+    // Gradients of 16 or 32 places take 32 ranks at most: with 64 and both orders of a matrix the
+    // registers leave one workgroup a CU (8192 rows, rank 128, 4096 x 4096: 250 against 261 us),
+    // which pays with 64 places only (below).
     y.rt = y.mt == 1 && y.slots * blocks <= 1024 ? 1 : blocks >= 4 && !grad ? 4 : blocks >= 2 ? 2 : 1;
     // 64 places by 64 ranks where that makes a workgroup for each CU (8192 rows, rank 64, K = 4096,
     // 133 of them: 30 us, with 32 places 25).

@@ -486,7 +486,9 @@ __global__ __launch_bounds__(256) void combine_kernel(RowsArgs a) {
     store8<T>(a.out, p.token * a.ldo + col, left, sum);
 }
 
-// Past the caches, 16384 rows of 4096 fp16: 62 against 65 us, of 2050: 39 against 50.
+// Past the caches, 16396 rows of 2050 fp16: 35.2 against 37.7 us; of 4096 bf16 53 against 51.6.  In
+// fp32 a lane's two pieces lie 32 bytes from its neighbours', and 10 % more is written than the
+// rows hold: 129 against 120 us for 16384 rows of 4096.
 template <int T>
 __device__ __forceinline__ void store8_past(char *base, int64_t i, const float *x) {
     constexpr int ES = Raw8<T>::ES;
@@ -625,7 +627,7 @@ void launch_combine(RowsArgs a, int64_t tokens, hipStream_t s) {
         launch_combine_grad<T, 1>(a, tokens, s);
     } else if (a.cols <= 1024) {
         launch_combine_grad<T, 2>(a, tokens, s);
-    } else {  // 8 waves: 16384 rows of 4096 fp16 in 74 us, of 2050 in 50
+    } else {  // 16384 rows of 4096 bf16 in 53 us, 16396 of 2050 fp16 in 35
         launch_combine_grad<T, 4>(a, tokens, s);
     }
 }
